@@ -228,6 +228,64 @@ colibri_status colibri_combine(const void* Yp, int32_t act_dtype, const int32_t*
                                void* y, void* stream);
 
 /*
+ * int8 products -- rows of activations and weights both in int8, with one fp32 scale per row
+ * (token) and one per output channel (www.0539edu.com/news/4774449 §3.1 quantises the expert
+ * weights; here the activations are rounded to int8 too, so a product runs on the int8 tensor
+ * cores once).  No context, no device allocation; all buffers are caller-owned device memory of
+ * the current device, 16-byte aligned; outputs must not overlap inputs.  Work is enqueued on
+ * `stream`; calls may overlap on the GPU.  Row strides (ld*) are in elements; the rows of x, q, A
+ * and W must start on 16-byte boundaries, those of y need not.  K (cols) is a multiple of 16, up
+ * to 131056 (the int32 sums are exact); N up to 2^20, rows up to 2^24; zero rows launch nothing.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA; reason via colibri_last_error(NULL).
+ *
+ * colibri_quantize_rows -- per row r of x [rows, cols] (act_dtype F32 or BF16):
+ *   scale[r] = max |x[r][:]| / 127 in fp32; q[r][c] = the integer nearest to the exact quotient
+ *   x[r][c] / scale[r], halves to even.  A row whose scale would be below 2^-126 (all zeros) gets
+ *   scale 1 and zeros.  A row that holds a NaN or an infinity gets scale NaN and zeros, so that
+ *   every product with it is NaN.
+ */
+colibri_status colibri_quantize_rows(const void* x, int32_t act_dtype, int32_t rows, int32_t cols,
+                                     int64_t ldx, int8_t* q, int64_t ldq, float* scale,
+                                     void* stream);
+
+/*
+ * colibri_int_gemm -- y[m][n] = a_scale[m] * w_scale[n] * sum_k A[m][k] * W[n][k] for A [M, K],
+ * W [N, K] (rows = output channels), y [M, N] in out_dtype (F32 or BF16).
+ */
+colibri_status colibri_int_gemm(const int8_t* A, int64_t lda, const float* a_scale,
+                                const int8_t* W, int64_t ldw, const float* w_scale, int32_t M,
+                                int32_t N, int32_t K, void* y, int64_t ldy, int32_t out_dtype,
+                                void* stream);
+
+/*
+ * colibri_int_gemm_experts -- the same product for rows grouped by expert
+ * (www.trdm.cn/news/555962 §6.2): rows [offsets[e], offsets[e+1]) of A [rows, K] meet the [N, K]
+ * weights at W + e * w_stride (elements, a multiple of 16) and the N scales at
+ * w_scale + e * s_stride.  offsets [num_experts + 1] is read on the device, so that it may come
+ * from the Scatter stage; num_experts 1..256.  It should ascend within [0, rows]; entry i counts
+ * as the largest of entries 0..i, limited to that range.  Rows outside every group are left as
+ * they were.
+ */
+colibri_status colibri_int_gemm_experts(const int8_t* A, int64_t lda, const float* a_scale,
+                                        int32_t rows, const int32_t* offsets, int32_t num_experts,
+                                        const int8_t* W, int64_t w_stride, const float* w_scale,
+                                        int64_t s_stride, int32_t N, int32_t K, void* y,
+                                        int64_t ldy, int32_t out_dtype, void* stream);
+
+/*
+ * colibri_int_swiglu_experts -- the gate and up projections in one call: expert e holds
+ * W1 [N, K] | W3 [N, K] and scales s1 [N] | s3 [N] (the start of the expert weight buffer's int8
+ * layout); g and u are the two products in fp32 and h[r][n] = silu(g) * u.  Other arguments as
+ * colibri_int_gemm_experts.
+ */
+colibri_status colibri_int_swiglu_experts(const int8_t* A, int64_t lda, const float* a_scale,
+                                          int32_t rows, const int32_t* offsets,
+                                          int32_t num_experts, const int8_t* W, int64_t w_stride,
+                                          const float* w_scale, int64_t s_stride, int32_t N,
+                                          int32_t K, void* h, int64_t ldh, int32_t out_dtype,
+                                          void* stream);
+
+/*
  * colibri_sync_status -- synchronise `stream`, then read and clear the context's device
  * error word.  Returns COLIBRI_ERR_TIMEOUT if a kernel's bounded wait gave up since the last
  * check (its output is then undefined), COLIBRI_ERR_CUDA if the stream reports an error,

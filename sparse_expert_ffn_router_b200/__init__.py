@@ -38,6 +38,10 @@ EXPORTS = (
     "colibri_moe_forward_routed",
     "colibri_get_routing",
     "colibri_combine",
+    "colibri_quantize_rows",
+    "colibri_int_gemm",
+    "colibri_int_gemm_experts",
+    "colibri_int_swiglu_experts",
     "colibri_sync_status",
     "colibri_profile_begin",
     "colibri_profile_end",
@@ -98,6 +102,13 @@ def load() -> ctypes.CDLL:
     lib.colibri_get_routing.restype = ctypes.c_int
     lib.colibri_combine.argtypes = [vp, i32, vp, vp, i32, i32, i32, vp, vp]
     lib.colibri_combine.restype = ctypes.c_int
+    lib.colibri_quantize_rows.argtypes = [vp, i32, i32, i32, i64, vp, i64, vp, vp]
+    lib.colibri_quantize_rows.restype = ctypes.c_int
+    lib.colibri_int_gemm.argtypes = [vp, i64, vp, vp, i64, vp, i32, i32, i32, vp, i64, i32, vp]
+    lib.colibri_int_gemm.restype = ctypes.c_int
+    for f in (lib.colibri_int_gemm_experts, lib.colibri_int_swiglu_experts):
+        f.argtypes = [vp, i64, vp, i32, vp, i32, vp, i64, vp, i64, i32, i32, vp, i64, i32, vp]
+        f.restype = ctypes.c_int
     lib.colibri_sync_status.argtypes = [vp, vp]
     lib.colibri_sync_status.restype = ctypes.c_int
     lib.colibri_profile_begin.argtypes = [vp, i32]
@@ -193,6 +204,35 @@ def colibri_combine(Yp, act_dtype: int, dst_row, topk_w, T: int, top_k: int, d_m
     """Gather stage alone: y[t] = sum_j topk_w[t][j] * Yp[dst_row[t][j]] (see include/colibri.h)."""
     _check(load().colibri_combine(_addr(Yp), act_dtype, _addr(dst_row), _addr(topk_w), T, top_k, d_model, _addr(y),
                                   _stream(stream)), "colibri_combine")
+
+
+def colibri_quantize_rows(x, act_dtype: int, rows: int, cols: int, ldx: int, q, ldq: int, scale, stream=None) -> None:
+    """int8 rows with one scale per row (see include/colibri.h)."""
+    _check(load().colibri_quantize_rows(_addr(x), act_dtype, rows, cols, ldx, _addr(q), ldq, _addr(scale),
+                                        _stream(stream)), "colibri_quantize_rows")
+
+
+def colibri_int_gemm(A, lda: int, a_scale, W, ldw: int, w_scale, M: int, N: int, K: int, y, ldy: int,
+                     out_dtype: int, stream=None) -> None:
+    """y[m][n] = a_scale[m] * w_scale[n] * sum_k A[m][k] W[n][k] in int8 (see include/colibri.h)."""
+    _check(load().colibri_int_gemm(_addr(A), lda, _addr(a_scale), _addr(W), ldw, _addr(w_scale), M, N, K, _addr(y),
+                                   ldy, out_dtype, _stream(stream)), "colibri_int_gemm")
+
+
+def colibri_int_gemm_experts(A, lda: int, a_scale, rows: int, offsets, num_experts: int, W, w_stride: int, w_scale,
+                             s_stride: int, N: int, K: int, y, ldy: int, out_dtype: int, stream=None) -> None:
+    """The int8 product for rows grouped by expert (see include/colibri.h)."""
+    _check(load().colibri_int_gemm_experts(_addr(A), lda, _addr(a_scale), rows, _addr(offsets), num_experts, _addr(W),
+                                           w_stride, _addr(w_scale), s_stride, N, K, _addr(y), ldy, out_dtype,
+                                           _stream(stream)), "colibri_int_gemm_experts")
+
+
+def colibri_int_swiglu_experts(A, lda: int, a_scale, rows: int, offsets, num_experts: int, W, w_stride: int, w_scale,
+                               s_stride: int, N: int, K: int, h, ldh: int, out_dtype: int, stream=None) -> None:
+    """Gate and up products with h = silu(g) * u for rows grouped by expert (see include/colibri.h)."""
+    _check(load().colibri_int_swiglu_experts(_addr(A), lda, _addr(a_scale), rows, _addr(offsets), num_experts,
+                                             _addr(W), w_stride, _addr(w_scale), s_stride, N, K, _addr(h), ldh,
+                                             out_dtype, _stream(stream)), "colibri_int_swiglu_experts")
 
 
 def colibri_sync_status(ctx: int, stream=None) -> None:

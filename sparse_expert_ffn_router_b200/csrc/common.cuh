@@ -357,6 +357,32 @@ struct DecFusedArgs {
 constexpr int kFusedBarCount = 8;
 cudaError_t launch_dec_fused(const DecFusedArgs& a, cudaStream_t s);
 
+// ---- int8 products (gemm_i8.cu) and the rows they read (quantize.cu)
+constexpr int kIntMaxK = 131056;       // K * 128 * 128 < 2^31: the int32 sums cannot overflow
+constexpr int kIntMaxN = 1 << 20;
+constexpr int kIntMaxRows = 1 << 24;
+constexpr int64_t kIntMaxLd = (1ll << 31) - 1;
+constexpr int64_t kIntMaxStride = 1ll << 38;
+struct IntGemmArgs {
+  const int8_t* A;         // [rows, K], row stride lda
+  int64_t lda;
+  const float* a_scale;    // [rows]
+  int rows;
+  const int32_t* offsets;  // [E+1] device: rows of expert e; nullptr: one group of all rows
+  int E;
+  const int8_t* W;         // expert e at e * w_stride: [N, K] (SwiGLU: W1 [N, K] | W3 [N, K]), row stride ldw
+  int64_t w_stride, ldw;
+  const float* w_scale;    // expert e at e * s_stride: [N] (SwiGLU: [N] | [N])
+  int64_t s_stride;
+  int N, K;
+  void* y;                 // [rows, N], row stride ldy
+  int64_t ldy;
+  int out_dtype;           // COLIBRI_F32 or COLIBRI_BF16
+};
+cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s);
+cudaError_t launch_quantize_rows(const void* x, int act, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,
+                                 float* scale, cudaStream_t s);
+
 // ---------------------------------------------------------------------------------------
 // Small device helpers
 // ---------------------------------------------------------------------------------------

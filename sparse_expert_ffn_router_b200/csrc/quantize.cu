@@ -1,0 +1,164 @@
+// Rows of activations as int8 with one fp32 scale per row, the left operand of the int8 products
+// (gemm_i8.cu):
+//
+//   top = max_k |x[k]|,  s = fl32(top / 127),  q[k] = the integer nearest to x[k] / s, halves to even
+//
+// q is the rounding of the exact quotient, not of a rounded one: h = rint(x * fl(1 / s)) is within
+// one of it (|x / s| <= 127, so the product is off by less than 127 * 2^-22), and the remainder
+// r = x - h s has no rounding error in fp32 (it is a multiple of the smaller of the two ulps and
+// at most about s / 2), so comparing 2 |r| with s settles the last step, ties included.  The
+// result therefore does not depend on how a division is carried out.
+//
+// A row whose s would be below 2^-126 (all zeros, or nothing above 127 * 2^-126) gets s = 1 and
+// zeros.  A row that holds a NaN or an infinity gets s = NaN and zeros: every product with it is
+// then NaN, as the row's own values would have made it.
+//
+// Bound by memory: a row is read once, kept in registers while its maximum is formed, and written
+// once (3 bytes per bf16 element).  Each thread owns units of 16 elements (two or four 16-byte
+// loads, one 16-byte store).
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace colibri {
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr int kQUnits = 4;  // units of 16 elements a thread keeps in registers
+
+template <typename T>
+struct Unit16 {  // 16 consecutive elements of a row
+  uint4 v[sizeof(T)];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ float get(int i) const;
+};
+template <>
+__device__ __forceinline__ float Unit16<__nv_bfloat16>::get(int i) const {
+  const uint4& q = v[i >> 3];
+  const int j = (i >> 1) & 3;
+  const uint32_t w = j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w;
+  return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+}
+template <>
+__device__ __forceinline__ float Unit16<float>::get(int i) const {
+  const uint4& q = v[i >> 2];
+  const int j = i & 3;
+  return __uint_as_float(j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w);
+}
+
+// Largest magnitude as the bits of a non-negative float: their order as integers is the order of
+// the values, and infinities and NaNs come out above every finite value.
+template <typename T>
+__device__ __forceinline__ uint32_t unit_top(const Unit16<T>& u) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(u.get(i)) & 0x7fffffffu);
+  return m;
+}
+
+__device__ __forceinline__ int quotient(float x, float s, float inv) {
+  float h = rintf(x * inv);
+  const float r = fmaf(-h, s, x);
+  const float r2 = 2.f * fabsf(r);
+  if (r2 > s || (r2 == s && ((int)h & 1))) h += copysignf(1.f, r);
+  return (int)h;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 unit_quantize(const Unit16<T>& u, float s, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)quotient(u.get(4 * i + j), s, inv) & 0xffu) << (8 * j);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// TPR threads per row (32, or the whole CTA)
+template <typename T, int TPR>
+__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* __restrict__ x, int rows, int units,
+                                                                  int64_t ldx, int8_t* __restrict__ q, int64_t ldq,
+                                                                  float* __restrict__ scale) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kRows = kQThreads / TPR;
+  __shared__ uint32_t part[kQThreads / 32];
+  const int t = threadIdx.x % TPR;
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
+    const int64_t r = r0 + threadIdx.x / TPR;
+    const bool live = r < rows;
+    const T* src = x + (live ? r : 0) * ldx;
+    Unit16<T> u[kQUnits];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kQUnits; ++i)
+      if (live && t + i * TPR < units) u[i].load(src + (size_t)(t + i * TPR) * 16);
+#pragma unroll
+    for (int i = 0; i < kQUnits; ++i)
+      if (live && t + i * TPR < units) top = max(top, unit_top(u[i]));
+    for (int c = t + kQUnits * TPR; live && c < units; c += TPR) {  // a row longer than the registers hold
+      Unit16<T> more;
+      more.load(src + (size_t)c * 16);
+      top = max(top, unit_top(more));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (TPR > 32) {
+      __syncthreads();  // the previous row's readers are done
+      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kQThreads / 32; ++i) top = max(top, part[i]);
+    }
+    const bool finite = top < 0x7f800000u;
+    float s = __fdiv_rn(__uint_as_float(top), 127.f);
+    bool zero = !finite;
+    if (finite && s < 1.17549435e-38f) {  // 2^-126
+      s = 1.f;
+      zero = true;
+    }
+    if (!finite) s = __uint_as_float(0x7fc00000u);
+    if (!live) continue;
+    if (t == 0) scale[r] = s;
+    const float inv = 1.f / s;
+    uint4* dst = reinterpret_cast<uint4*>(q + r * ldq);
+#pragma unroll
+    for (int i = 0; i < kQUnits; ++i)
+      if (t + i * TPR < units) dst[t + i * TPR] = zero ? make_uint4(0, 0, 0, 0) : unit_quantize(u[i], s, inv);
+    for (int c = t + kQUnits * TPR; c < units; c += TPR) {
+      Unit16<T> more;
+      more.load(src + (size_t)c * 16);
+      dst[c] = zero ? make_uint4(0, 0, 0, 0) : unit_quantize(more, s, inv);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_q(const T* x, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale, cudaStream_t s) {
+  const int units = cols / 16;
+  // a warp per row while its registers hold the row, else a CTA per row
+  if (units <= 32 * kQUnits) {
+    const int grid = std::min((rows + 7) / 8, 148 * 64);
+    return launch_kernel(quantize_rows_kernel<T, 32>, dim3(grid), dim3(kQThreads), 0, s, 1, x, rows, units, ldx, q, ldq,
+                         scale);
+  }
+  const int grid = std::min(rows, 148 * 64);
+  return launch_kernel(quantize_rows_kernel<T, kQThreads>, dim3(grid), dim3(kQThreads), 0, s, 1, x, rows, units, ldx, q,
+                       ldq, scale);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const void* x, int act, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,
+                                 float* scale, cudaStream_t s) {
+  if (rows <= 0) return cudaSuccess;
+  if (act == COLIBRI_BF16) return launch_q((const __nv_bfloat16*)x, rows, cols, ldx, q, ldq, scale, s);
+  return launch_q((const float*)x, rows, cols, ldx, q, ldq, scale, s);
+}
+
+}  // namespace colibri
