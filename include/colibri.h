@@ -194,6 +194,24 @@ colibri_status colibri_moe_forward_routed(colibri_ctx* ctx, const void* x, int32
                                           const void* shared_w, void* y, void* stream);
 
 /*
+ * colibri_moe_decode -- the same layer for a few tokens as one cooperative launch: y = MoE(x) for
+ * 0 <= T <= min(16, max_tokens) on a context with bf16 or fp32 weights (with or without a shared
+ * expert, any router_flags).  A call reads the touched experts' weights once and is bound by that
+ * stream; colibri_moe_forward runs the same layer as a sequence of launches tuned for many tokens.
+ * (www.hotelren.com/news/4731937 §2.1, the token-by-token step of generation.)  Arguments, host x
+ * and y, graph replay, the routing state left for colibri_get_routing and the stage events (all
+ * time counts as the gate/up stage) are those of colibri_moe_forward.  The two entry points agree
+ * within the rounding of their sums, not bit for bit; a call's result does not vary from run to
+ * run.  The launch needs every SM of the device for a CTA of 512 threads: beside other work it
+ * starts once they are free.  Errors: INVALID_ARG (also T > 16), ALIGNMENT, UNSUPPORTED (int8 and
+ * int4 weights, which colibri_moe_forward streams at these sizes), CUDA.
+ */
+colibri_status colibri_moe_decode(colibri_ctx* ctx, const void* x, int32_t T,
+                                  const void* router_w, const float* router_b,
+                                  const void* expert_w, const void* shared_w, void* y,
+                                  void* stream);
+
+/*
  * colibri_get_routing -- enqueue device-to-device copies of the routing state of the last
  * forward on this context into caller buffers (any pointer may be NULL to skip it).  The pages
  * have no counterpart of this call: it exposes the Gate and Scatter results (whose layouts follow

@@ -36,6 +36,7 @@ EXPORTS = (
     "colibri_expert_stride",
     "colibri_moe_forward",
     "colibri_moe_forward_routed",
+    "colibri_moe_decode",
     "colibri_get_routing",
     "colibri_combine",
     "colibri_quantize_rows",
@@ -98,6 +99,8 @@ def load() -> ctypes.CDLL:
     lib.colibri_moe_forward.restype = ctypes.c_int
     lib.colibri_moe_forward_routed.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
     lib.colibri_moe_forward_routed.restype = ctypes.c_int
+    lib.colibri_moe_decode.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp]
+    lib.colibri_moe_decode.restype = ctypes.c_int
     lib.colibri_get_routing.argtypes = [vp] * 8
     lib.colibri_get_routing.restype = ctypes.c_int
     lib.colibri_combine.argtypes = [vp, i32, vp, vp, i32, i32, i32, vp, vp]
@@ -191,6 +194,12 @@ def colibri_moe_forward_routed(ctx: int, x, T: int, topk_idx, topk_w, expert_w, 
     _check(load().colibri_moe_forward_routed(ctx, _addr(x), T, _addr(topk_idx), _addr(topk_w), _addr(expert_w),
                                              _addr(expert_scales), _addr(shared_w), _addr(y), _stream(stream)),
            "colibri_moe_forward_routed", ctx)
+
+
+def colibri_moe_decode(ctx: int, x, T: int, router_w, router_b, expert_w, shared_w, y, stream=None) -> None:
+    """The whole layer for at most 16 tokens in one launch (see include/colibri.h)."""
+    _check(load().colibri_moe_decode(ctx, _addr(x), T, _addr(router_w), _addr(router_b), _addr(expert_w),
+                                     _addr(shared_w), _addr(y), _stream(stream)), "colibri_moe_decode", ctx)
 
 
 def colibri_get_routing(ctx: int, topk_idx=None, topk_w=None, counts=None, offsets=None, src_row=None,
@@ -312,6 +321,11 @@ class MoELayer:
     def forward_routed(self, x, topk_idx, topk_w, expert_w, y, expert_scales=None, shared_w=None, stream=None):
         colibri_moe_forward_routed(self.ctx, x, x.shape[0], topk_idx, topk_w, expert_w, expert_scales, shared_w,
                                    y, stream)
+        return y
+
+    def decode(self, x, router_w, router_b, expert_w, y, shared_w=None, stream=None, T=None):
+        T = x.shape[0] if T is None else T
+        colibri_moe_decode(self.ctx, x, T, router_w, router_b, expert_w, shared_w, y, stream)
         return y
 
     def routing(self, **bufs):

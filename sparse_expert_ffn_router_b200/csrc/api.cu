@@ -87,7 +87,7 @@ int pick_dec_split(int f) {
 // operands, so the 256-row tile no longer pads small groups (measured on B200: the 128-expert
 // layer 678 against 711 us per step, the skewed layer 998 against 1027 us, the Mixtral-shaped
 // layer unchanged in mode).  COLIBRI_GEMM_CTA=1 or 2 forces a mode (both are exact).
-enum GemmMode { kGemmOne = 0, kGemmPair = 1 };
+enum GemmMode { kGemmOne = 0, kGemmPair = 1, kFewTokens = 2 };  // kFewTokens: no GEMMs, the one-launch layer
 int gemm_mode(int /*avg_rows_per_expert*/) {
   const char* v = getenv("COLIBRI_GEMM_CTA");
   if (v && v[0] == '1') return kGemmOne;
@@ -232,6 +232,7 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   const size_t o_psc = c.take(i8 ? part_rows * 4 : 0);  // per (down K split, row) scales of the H planes
   const size_t o_err = c.take(4);
   const size_t o_tsched = c.take(4 * 4);
+  const size_t o_flog = c.take(i8 ? 0 : std::min<int64_t>(M, kFewMaxT) * E * 4), o_fbar = c.take(i8 ? 0 : 2 * 4);
   const size_t o_gbar = c.take(i8 ? kFusedBarCount * 4 : 0);
   ctx->ws_bytes = c.off;
 
@@ -268,8 +269,11 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   w.plane_scale = reinterpret_cast<float*>(b + o_psc);
   w.err = reinterpret_cast<uint32_t*>(b + o_err);
   w.tile_sched = reinterpret_cast<uint32_t*>(b + o_tsched);
+  w.few_logits = reinterpret_cast<float*>(b + o_flog);
+  w.few_bar = i8 ? nullptr : reinterpret_cast<int32_t*>(b + o_fbar);
   w.grid_bar = i8 ? reinterpret_cast<int32_t*>(b + o_gbar) : nullptr;
   if (cudaMemset(w.err, 0, 4) != cudaSuccess || cudaMemset(w.tile_sched, 0, 4 * 4) != cudaSuccess ||
+      (!i8 && cudaMemset(w.few_bar, 0, 2 * 4) != cudaSuccess) ||
       (i8 && cudaMemset(w.grid_bar, 0, kFusedBarCount * 4) != cudaSuccess)) {
     cudaFree(ctx->ws_base);
     delete ctx;
@@ -298,6 +302,7 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   if (ce == cudaSuccess) ce = configure_tc_kernels();
   if (ce == cudaSuccess) ce = configure_dec_kernels();
   if (ce == cudaSuccess) ce = configure_simt_kernels();
+  if (ce == cudaSuccess) ce = configure_few_kernels();
   if (ce != cudaSuccess) {
     cudaGetLastError();
     cudaFree(ctx->ws_base);
@@ -355,6 +360,25 @@ colibri_status check_launch(colibri_ctx* ctx, cudaError_t e, const char* what) {
     if (st_ != COLIBRI_OK) return st_;                          \
   } while (0)
 
+// The end of a forward: the last stage mark, host y, and the printed stage times.
+template <typename Mark>
+colibri_status finish_forward(colibri_ctx* ctx, void* y, const void* yd, size_t bytes, PtrKind yk, int32_t T,
+                              cudaStream_t s, Mark& mark) {
+  mark(5);
+  if (yk == kPtrHost)
+    COLIBRI_TRY(cudaMemcpyAsync(y, yd, bytes, cudaMemcpyDeviceToHost, s), "copy y to host");
+
+  if (ctx->profile) {
+    cudaStreamSynchronize(s);
+    float ms[5] = {0, 0, 0, 0, 0}, tot = 0;
+    for (int i = 0; i < 5; ++i) cudaEventElapsedTime(&ms[i], ctx->ev[i], ctx->ev[i + 1]);
+    cudaEventElapsedTime(&tot, ctx->ev[0], ctx->ev[5]);
+    fprintf(stderr, "[colibri] T=%d Gate %.4f ms | Scatter %.4f ms | ExpertCompute %.4f ms | Gather %.4f ms | Total %.4f ms\n",
+            T, ms[0], ms[1], ms[2] + ms[3], ms[4], tot);
+  }
+  return COLIBRI_OK;
+}
+
 // The launch sequence of one forward (stream-ordered, no host synchronisation unless
 // COLIBRI_PROFILE printing is on).
 // stage_ev: NULL, or 6 events recorded at the stage boundaries (as event-record nodes when
@@ -390,6 +414,43 @@ colibri_status enqueue_forward(colibri_ctx* ctx, const void* x, PtrKind xk, int3
     }
   };
   mark(0);
+
+  if (gemm == kFewTokens) {
+    // the whole layer in one launch (counted as the gate/up stage)
+    FewArgs fa;
+    fa.x = xd;
+    fa.router_w = router_w;
+    fa.router_b = router_b;
+    fa.W = expert_w;
+    fa.wstride = ctx->expert_stride;
+    fa.W_sh = shared_w;
+    fa.H = w.H;
+    fa.Hs = w.Hs;
+    fa.y = yd;
+    fa.logits = w.few_logits;
+    fa.topk_idx = w.topk_idx;
+    fa.topk_w = w.topk_w;
+    fa.counts = w.counts;
+    fa.offsets = w.offsets;
+    fa.src_row = w.src_row;
+    fa.dst_row = w.dst_row;
+    fa.bar = w.few_bar;
+    fa.err = w.err;
+    fa.T = T;
+    fa.d = d;
+    fa.f = f;
+    fa.fs = fs;
+    fa.E = E;
+    fa.k = k;
+    fa.router_flags = D.router_flags;
+    fa.sm_count = ctx->sm_count;
+    mark(1);
+    mark(2);
+    COLIBRI_TRY(launch_few_tokens(fa, act, s), "few_tokens");
+    mark(3);
+    mark(4);
+    return finish_forward(ctx, y, yd, (size_t)T * row_bytes, yk, T, s, mark);
+  }
 
   // int8 weights, T <= 64: router, top-k and grouping run as phase 0 of the fused expert launch
   // (COLIBRI_DEC_ROUTE=0: as two launches before it).  With the weight streams evicted first
@@ -575,25 +636,13 @@ colibri_status enqueue_forward(colibri_ctx* ctx, const void* x, PtrKind xk, int3
     COLIBRI_TRY(launch_combine(w.Yp, yp_dtype, w.dst_row, w.topk_w, T, k, d, fs > 0 ? w.Ys : nullptr, yd, act, s),
                 "combine");
   }
-  mark(5);
-  if (yk == kPtrHost)
-    COLIBRI_TRY(cudaMemcpyAsync(y, yd, (size_t)T * row_bytes, cudaMemcpyDeviceToHost, s), "copy y to host");
-
-  if (ctx->profile) {
-    cudaStreamSynchronize(s);
-    float ms[5] = {0, 0, 0, 0, 0}, tot = 0;
-    for (int i = 0; i < 5; ++i) cudaEventElapsedTime(&ms[i], ctx->ev[i], ctx->ev[i + 1]);
-    cudaEventElapsedTime(&tot, ctx->ev[0], ctx->ev[5]);
-    fprintf(stderr, "[colibri] T=%d Gate %.4f ms | Scatter %.4f ms | ExpertCompute %.4f ms | Gather %.4f ms | Total %.4f ms\n",
-            T, ms[0], ms[1], ms[2] + ms[3], ms[4], tot);
-  }
-  return COLIBRI_OK;
+  return finish_forward(ctx, y, yd, (size_t)T * row_bytes, yk, T, s, mark);
 }
 
 colibri_status forward_device(colibri_ctx* ctx, const void* x, PtrKind xk, int32_t T, const void* router_w,
                               const float* router_b, const int32_t* user_idx, const float* user_w,
                               const void* expert_w, const float* expert_scales, const void* shared_w, void* y,
-                              PtrKind yk, cudaStream_t s);
+                              PtrKind yk, cudaStream_t s, bool few);
 
 bool stream_capturing(cudaStream_t s) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
@@ -615,7 +664,7 @@ bool stream_capturing(cudaStream_t s) {
 colibri_status forward_staged(colibri_ctx* ctx, const void* x, PtrKind xk, int32_t T, const void* router_w,
                               const float* router_b, const int32_t* user_idx, const float* user_w,
                               const void* expert_w, const float* expert_scales, const void* shared_w, void* y,
-                              PtrKind yk, cudaStream_t s) {
+                              PtrKind yk, cudaStream_t s, bool few) {
   const colibri_desc& D = ctx->desc;
   Workspace& w = ctx->ws;
   const size_t bytes = (size_t)T * D.d_model * (D.act_dtype == COLIBRI_F32 ? 4 : 2);
@@ -635,7 +684,7 @@ colibri_status forward_staged(colibri_ctx* ctx, const void* x, PtrKind xk, int32
   }
   if (yk == kPtrHost) yd = ys;
   const colibri_status st = forward_device(ctx, xd, kPtrDevice, T, router_w, router_b, user_idx, user_w, expert_w,
-                                           expert_scales, shared_w, yd, kPtrDevice, s);
+                                           expert_scales, shared_w, yd, kPtrDevice, s, few);
   if (st != COLIBRI_OK) return st;
   if (xk == kPtrHost) COLIBRI_TRY(cudaEventRecord(ev[0], s), "staged: record x buffer free");
   if (yk == kPtrHost) {
@@ -652,7 +701,7 @@ colibri_status forward_staged(colibri_ctx* ctx, const void* x, PtrKind xk, int32
 colibri_status forward_impl(colibri_ctx* ctx, const void* x, int32_t T, const void* router_w,
                             const float* router_b, const int32_t* user_idx, const float* user_w,
                             const void* expert_w, const float* expert_scales, const void* shared_w,
-                            void* y, void* stream_ptr) {
+                            void* y, void* stream_ptr, bool few = false) {
   if (!ctx) return fail(nullptr, COLIBRI_ERR_INVALID_ARG, "ctx is NULL");
   const colibri_desc& D = ctx->desc;
   const bool routed_by_caller = user_idx != nullptr || user_w != nullptr;
@@ -687,19 +736,20 @@ colibri_status forward_impl(colibri_ctx* ctx, const void* x, int32_t T, const vo
     return fail(ctx, COLIBRI_ERR_INVALID_ARG, "x or y is device memory of another device");
   if ((xk == kPtrHost || yk == kPtrHost) && ctx->staged && !ctx->profile && !stream_capturing(s))
     return forward_staged(ctx, x, xk, T, router_w, router_b, user_idx, user_w, expert_w, expert_scales, shared_w, y,
-                          yk, s);
+                          yk, s, few);
   return forward_device(ctx, x, xk, T, router_w, router_b, user_idx, user_w, expert_w, expert_scales, shared_w, y,
-                        yk, s);
+                        yk, s, few);
 }
 
 // The forward once x and y are classified: a replayed graph when possible, else the launches.
 colibri_status forward_device(colibri_ctx* ctx, const void* x, PtrKind xk, int32_t T, const void* router_w,
                               const float* router_b, const int32_t* user_idx, const float* user_w,
                               const void* expert_w, const float* expert_scales, const void* shared_w, void* y,
-                              PtrKind yk, cudaStream_t s) {
+                              PtrKind yk, cudaStream_t s, bool few) {
   const colibri_desc& D = ctx->desc;
   // bf16 weights: the tiling of the expert GEMMs (see gemm_mode)
-  const int gemm = D.weight_dtype == COLIBRI_BF16 ? gemm_mode(T * D.top_k / D.num_experts) : kGemmOne;
+  const int gemm = few ? kFewTokens
+                       : (D.weight_dtype == COLIBRI_BF16 ? gemm_mode(T * D.top_k / D.num_experts) : kGemmOne);
 
   // Stage events of colibri_profile_begin: the events of this call, if it is still recorded.
   const bool prof_rec = ctx->prof_on && ctx->prof_n < ctx->prof_max;
@@ -815,6 +865,17 @@ colibri_status colibri_moe_forward_routed(colibri_ctx* ctx, const void* x, int32
                       stream);
 }
 
+colibri_status colibri_moe_decode(colibri_ctx* ctx, const void* x, int32_t T, const void* router_w,
+                                  const float* router_b, const void* expert_w, const void* shared_w, void* y,
+                                  void* stream) {
+  if (!ctx) return fail(nullptr, COLIBRI_ERR_INVALID_ARG, "ctx is NULL");
+  if (ctx->desc.weight_dtype != COLIBRI_F32 && ctx->desc.weight_dtype != COLIBRI_BF16)
+    return fail(ctx, COLIBRI_ERR_UNSUPPORTED, "colibri_moe_decode needs bf16 or fp32 weights (colibri_moe_forward "
+                "runs quantised layers in one launch at these sizes)");
+  if (T > kFewMaxT) return fail(ctx, COLIBRI_ERR_INVALID_ARG, "T=%d above %d tokens", T, kFewMaxT);
+  return forward_impl(ctx, x, T, router_w, router_b, nullptr, nullptr, expert_w, nullptr, shared_w, y, stream, true);
+}
+
 colibri_status colibri_get_routing(colibri_ctx* ctx, int32_t* topk_idx, float* topk_w, int32_t* counts,
                                    int32_t* offsets, int32_t* src_row, int32_t* dst_row, void* stream) {
   if (!ctx) return fail(nullptr, COLIBRI_ERR_INVALID_ARG, "ctx is NULL");
@@ -876,6 +937,7 @@ colibri_status colibri_sync_status(colibri_ctx* ctx, void* stream) {
     // a wait that gave up may leave the fused kernel's grid-barrier counters out of step
     if (ctx->ws.grid_bar)
       COLIBRI_TRY(cudaMemset(ctx->ws.grid_bar, 0, kFusedBarCount * 4), "reset grid-barrier counters");
+    if (ctx->ws.few_bar) COLIBRI_TRY(cudaMemset(ctx->ws.few_bar, 0, 2 * 4), "reset grid-barrier counters");
     COLIBRI_TRY(cudaMemset(ctx->ws.tile_sched, 0, 4 * 4), "reset tile counters");
     return fail(ctx, COLIBRI_ERR_TIMEOUT, "device error word 0x%x (a bounded wait gave up)", err);
   }

@@ -81,6 +81,8 @@ struct Workspace {
   int8_t* plane_lo = nullptr;
   float* plane_scale = nullptr;  // [M*k]
   uint32_t* err = nullptr;
+  float* few_logits = nullptr;   // [min(M, kFewMaxT), E] few-token path
+  int32_t* few_bar = nullptr;    // [2] its grid-barrier counters (zero at first use)
   uint32_t* tile_sched = nullptr;  // [4] tile counters of the bf16 GEMMs (gate/up, down; zero between calls)
 };
 
@@ -357,6 +359,29 @@ struct DecFusedArgs {
 constexpr int kFusedBarCount = 8;
 cudaError_t launch_dec_fused(const DecFusedArgs& a, cudaStream_t s);
 
+// ---- the whole layer for a few tokens in one launch (few_tokens.cu)
+constexpr int kFewMaxT = 16;
+struct FewArgs {
+  const void* x;           // [T, d] act
+  const void* router_w;    // [E, d] act
+  const float* router_b;   // [E] or nullptr
+  const void* W;           // expert buffer (act type)
+  int64_t wstride;
+  const void* W_sh;        // shared expert or nullptr (fs == 0)
+  void* H;                 // [T*k, f] act
+  void* Hs;                // [T, fs] act
+  void* y;                 // [T, d] act
+  float* logits;           // [T, E]
+  int32_t* topk_idx;       // routing state as every forward leaves it
+  float* topk_w;
+  int32_t *counts, *offsets, *src_row, *dst_row;
+  int32_t* bar;            // [2] grid-barrier counters: zero at first use, then owned by the kernel
+  uint32_t* err;
+  int T, d, f, fs, E, k, router_flags, sm_count;
+};
+cudaError_t configure_few_kernels();  // once per device, before any launch
+cudaError_t launch_few_tokens(const FewArgs& a, int act, cudaStream_t s);
+
 // ---- int8 products (gemm_i8.cu) and the rows they read (quantize.cu)
 constexpr int kIntMaxK = 131056;       // K * 128 * 128 < 2^31: the int32 sums cannot overflow
 constexpr int kIntMaxN = 1 << 20;
@@ -579,6 +604,53 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     if (mbar_try_wait(bar, parity)) return true;
     if ((++n & 255u) == 0 && global_ns() - t0 > kWaitTimeoutNs) return false;
   }
+}
+
+// ---------------------------------------------------------------------------------------
+// Grid barriers of the cooperative kernels
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ int ld_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Grid barriers are never reset.  A counter runs through [0, G * kBarLaps) (atom.inc wraps it
+// to 0), and every launch that uses it adds exactly G: each CTA arrives once, also after an
+// error.  A CTA's arrival returns the count before it; the round it belongs to started at the
+// multiple of G below that, and the barrier is passed once the counter has moved G beyond that
+// start.  The arrival (one thread, after a CTA barrier) is an acquire-release RMW, so every write
+// the CTA made before its CTA barrier is visible to a CTA that acquires the counter later.
+constexpr uint32_t kBarLaps = 1u << 16;
+__device__ __forceinline__ uint32_t bar_arrive(int32_t* ctr, int G) {  // returns the count before
+  uint32_t old;
+  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+               : "=r"(old)
+               : "l"(ctr), "r"((uint32_t)G * kBarLaps - 1u)
+               : "memory");
+  return old;
+}
+__device__ __forceinline__ uint32_t bar_base(uint32_t old, int G) { return old - old % (uint32_t)G; }
+__device__ __forceinline__ bool bar_passed(const int32_t* ctr, uint32_t base, int G) {
+  const uint32_t wrap = (uint32_t)G * kBarLaps;
+  return ((uint32_t)ld_acquire(ctr) + wrap - base) % wrap >= (uint32_t)G;
+}
+
+// Wait (bounded) until the round of the barrier `ctr` that started at `base` is complete.
+__device__ __forceinline__ bool grid_wait(const int32_t* ctr, uint32_t base, int G, volatile int* abort_flag) {
+  const unsigned long long t0 = global_ns();
+  while (!bar_passed(ctr, base, G)) {
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kWaitTimeoutNs) return false;
+    __nanosleep(64);
+  }
+  return true;
+}
+// Arrive and wait; the last CTA to arrive completes the round and does not wait.
+__device__ __forceinline__ bool grid_sync(int32_t* ctr, int G, volatile int* abort_flag) {
+  const uint32_t old = bar_arrive(ctr, G), base = bar_base(old, G);
+  if (old - base == (uint32_t)G - 1u) return true;
+  return grid_wait(ctr, base, G, abort_flag);
 }
 
 // ---------------------------------------------------------------------------------------

@@ -969,33 +969,6 @@ constexpr int kRedundantT = 1;
 enum { kBarRouter = 0, kBarPlanes, kBarGU, kBarH, kBarY, kFusedBars };
 static_assert(kFusedBars <= kFusedBarCount, "grid-barrier counters of the fused kernel");
 
-__device__ __forceinline__ int ld_acquire(const int32_t* p) {
-  int v;
-  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-
-// Grid barriers are never reset.  A counter runs through [0, G * kBarLaps) (atom.inc wraps it
-// to 0), and every launch that uses it adds exactly G: each CTA arrives once, also after an
-// error.  A CTA's arrival returns the count before it; the round it belongs to started at the
-// multiple of G below that, and the barrier is passed once the counter has moved G beyond that
-// start.  The arrival (one thread, after a CTA barrier) is an acquire-release RMW, so every write
-// the CTA made before its CTA barrier is visible to a CTA that acquires the counter later.
-constexpr uint32_t kBarLaps = 1u << 16;
-__device__ __forceinline__ uint32_t bar_arrive(int32_t* ctr, int G) {  // returns the count before
-  uint32_t old;
-  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
-               : "=r"(old)
-               : "l"(ctr), "r"((uint32_t)G * kBarLaps - 1u)
-               : "memory");
-  return old;
-}
-__device__ __forceinline__ uint32_t bar_base(uint32_t old, int G) { return old - old % (uint32_t)G; }
-__device__ __forceinline__ bool bar_passed(const int32_t* ctr, uint32_t base, int G) {
-  const uint32_t wrap = (uint32_t)G * kBarLaps;
-  return ((uint32_t)ld_acquire(ctr) + wrap - base) % wrap >= (uint32_t)G;
-}
-
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // A flag in shared memory passed from one role of the CTA to another.
@@ -1006,23 +979,6 @@ __device__ __forceinline__ int ld_acquire_cta(const int* p) {
 }
 __device__ __forceinline__ void st_release_cta(int* p, int v) {
   asm volatile("st.release.cta.shared.b32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
-}
-
-// Wait (bounded) until the round of the barrier `ctr` that started at `base` is complete.
-__device__ bool grid_wait(const int32_t* ctr, uint32_t base, int G, volatile int* abort_flag) {
-  const unsigned long long t0 = global_ns();
-  while (!bar_passed(ctr, base, G)) {
-    if (*abort_flag) return false;
-    if (global_ns() - t0 > kWaitTimeoutNs) return false;
-    __nanosleep(64);
-  }
-  return true;
-}
-// Arrive and wait; the last CTA to arrive completes the round and does not wait.
-__device__ bool grid_sync(int32_t* ctr, int G, volatile int* abort_flag) {
-  const uint32_t old = bar_arrive(ctr, G), base = bar_base(old, G);
-  if (old - base == (uint32_t)G - 1u) return true;
-  return grid_wait(ctr, base, G, abort_flag);
 }
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
