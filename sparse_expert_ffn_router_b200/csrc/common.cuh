@@ -637,20 +637,23 @@ __device__ __forceinline__ bool bar_passed(const int32_t* ctr, uint32_t base, in
 }
 
 // Wait (bounded) until the round of the barrier `ctr` that started at `base` is complete.
+// kSleepNs: pause between two looks at the counter (0: none, the lowest latency).
+template <unsigned kSleepNs = 64>
 __device__ __forceinline__ bool grid_wait(const int32_t* ctr, uint32_t base, int G, volatile int* abort_flag) {
   const unsigned long long t0 = global_ns();
   while (!bar_passed(ctr, base, G)) {
     if (*abort_flag) return false;
     if (global_ns() - t0 > kWaitTimeoutNs) return false;
-    __nanosleep(64);
+    if (kSleepNs) __nanosleep(kSleepNs);
   }
   return true;
 }
 // Arrive and wait; the last CTA to arrive completes the round and does not wait.
+template <unsigned kSleepNs = 64>
 __device__ __forceinline__ bool grid_sync(int32_t* ctr, int G, volatile int* abort_flag) {
   const uint32_t old = bar_arrive(ctr, G), base = bar_base(old, G);
   if (old - base == (uint32_t)G - 1u) return true;
-  return grid_wait(ctr, base, G, abort_flag);
+  return grid_wait<kSleepNs>(ctr, base, G, abort_flag);
 }
 
 // ---------------------------------------------------------------------------------------

@@ -18,16 +18,18 @@
 // The shares are split to single columns (a partly filled last tile loads only its own rows), so
 // that no CTA reads more than one row above the average.
 //
-// Inside a CTA the 16 warps split the inner dimension and each keeps its weights in flight through
-// a ring of shared memory that the same lane fills (cp.async) and drains: no lane reads what
-// another lane copied, so the ring needs no barrier, and a warp's copies run ahead across tiles,
-// experts and the barrier between the two projections.  bf16: mma.m16n8k16, weights as the 16-row
-// operand (8 gate rows and the 8 up rows of the same columns; for down 16 output columns), tokens
-// as the 8 columns; the order of k inside an instruction is free, so a lane's 16 bytes of a weight
-// row feed two instructions as they are, and the token operand is 16 bytes of the token's row.
-// fp32: FMA on the CUDA cores.  Partial sums of the warps meet in shared memory once per tile, in
-// warp order.  H is kept in the activation type between the projections (bf16: rounded once), as
-// on the library's other paths.
+// Inside a CTA the 16 warps split the inner dimension: all tiles' chunks of 64 bytes of a row, laid
+// end to end, go to the warps in equal runs, so a warp crosses tiles and experts without meeting the
+// others.  Partial sums meet in shared memory, in warp order, once per 16 tiles (gate/up) or once per
+// 32 output columns (down: a warp adds its experts up in registers, the columns of its partial sums
+// being the tokens).  Each lane keeps its weights in flight through a ring of shared memory that the
+// same lane fills (cp.async) and drains: no lane reads what another lane copied, so the ring needs
+// no barrier, and a warp's copies run ahead across tiles, experts and the barrier between the two
+// projections.  bf16: mma.m16n8k16, weights as the 16-row operand (8 gate rows and the 8 up rows of
+// the same columns; for down 16 output columns), tokens as the 8 columns; the order of k inside an
+// instruction is free, so a lane's 16 bytes of a weight row feed two instructions as they are, and
+// the token operand is 16 bytes of the token's row.  fp32: FMA on the CUDA cores.  H is kept in the
+// activation type between the projections (bf16: rounded once), as on the library's other paths.
 #include "common.cuh"
 
 namespace colibri {
@@ -40,6 +42,8 @@ constexpr int kFewRowsW = 32;            // weight rows of a tile: 4 per lane
 constexpr int kFewStage = 4 * 512;       // bytes of a warp's stage: 4 rows of 16 bytes per lane
 constexpr int kFewEntries = kFewMaxT * kMaxTopK + 1;  // touched experts and the shared one
 constexpr int kFewPitch = kFewMaxT + 2;  // floats per weight row of the partial sums (16 token columns)
+constexpr int kFewBatch = 16;            // gate/up tiles whose partial sums meet at a time
+constexpr int kFewSlot = kFewRowsW * kFewPitch;       // floats of one warp's partial sums of one tile
 
 struct FewCtl {
   int32_t idx[kFewMaxT * kMaxTopK];
@@ -50,18 +54,22 @@ struct FewCtl {
   int32_t ent_e[kFewEntries];            // expert, or -1: shared
   int32_t ent_row[kFewEntries];          // first row in H (shared: Hs)
   int32_t ent_n[kFewEntries];            // tokens
+  uint32_t ent_mask[kFewEntries];
   uint8_t ent_tok[kFewEntries][kFewMaxT];
+  float ent_w[kFewEntries][kFewMaxT];    // weight by token
   int32_t n_ent;
   int32_t ok;
   int32_t abort;
   float part[kFewWarps][kFewMaxT];       // router partial sums
-  float yacc[kFewMaxT][kFewRowsW];
 };
 
+// the tiles of a batch are consecutive, and so are the warps' runs over them: the partial sums of
+// (tile i, warp w) go to slot i + w
 constexpr size_t kFewRing = (size_t)kFewWarps * kFewDepth * kFewStage;
-constexpr size_t kFewRed = (size_t)kFewWarps * kFewRowsW * kFewPitch * 4;  // one of two
-constexpr size_t kFewSmem = kFewRing + 2 * kFewRed + sizeof(FewCtl);
+constexpr size_t kFewRed = (size_t)(kFewBatch + kFewWarps - 1) * kFewSlot * 4;
+constexpr size_t kFewSmem = kFewRing + kFewRed + sizeof(FewCtl);
 static_assert(kFewSmem <= 232448, "shared memory of the few-token kernel");
+static_assert((size_t)kFewMaxT * kMaxExperts * 4 <= kFewRed, "logits are staged in the partial sums' memory");
 
 template <typename T>
 struct FewParams {
@@ -80,10 +88,11 @@ struct FewParams {
   int32_t* bar;        // [2]
   uint32_t* err;
   int T_, d, f, fs, E, k, flags;
+  int tg;              // router: tokens per task
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -98,129 +107,149 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One CTA's sequence of tiles.  Phase 0 (gate/up): columns [c0, c1) of all entries' gate columns
-// laid end to end, in tiles of at most 16 columns of one entry.  Phase 1 (down): output columns
-// [o0, o1) in groups of 32, every entry in turn per group.
+// The runs of chunks of one CTA.  Gate/up: the gate columns of all entries laid end to end, cut into
+// tiles of 16 (every width is a multiple of 64, so a tile lies in one entry); the CTA owns columns
+// [c0, c1) and takes their tiles in batches.  Down: the CTA owns output columns [o0, o1), in groups of
+// 32, each group over the chunks of all entries laid end to end.
 template <typename T>
-struct FewWalk {
-  const FewParams<T>& p;
-  const FewCtl& c;
-  int phase;  // 2: no tiles left
-  int ent, col, n;  // current tile: entry, first column, columns
-  int64_t c1;       // phase 0: end of the CTA's share, counted from the current entry's column 0
-  int o1;
+struct FewShare {
+  static constexpr int CE = 64 / sizeof(T);  // elements of a chunk
+  int c0, c1;
+  int o0, o1;
+  int tiles, batches, groups;
+  int cd, cf, cs;  // chunks of a row of d, f, fs elements
+  int down_chunks;
+  int fs, f;
 
-  __device__ FewWalk(const FewParams<T>& p_, const FewCtl& c_) : p(p_), c(c_), phase(0), ent(0) {
-    const int G = gridDim.x, b = blockIdx.x;
-    const int64_t total = (int64_t)p.fs + (int64_t)(c.n_ent - (p.fs > 0 ? 1 : 0)) * p.f;
-    int64_t at = total * b / G;
-    c1 = total * (b + 1) / G;
-    while (ent < c.n_ent && at >= width()) {
-      at -= width();
-      c1 -= width();
-      ++ent;
-    }
-    col = (int)at;
-    settle();
+  __device__ FewShare(const FewParams<T>& p, int n_ent) {
+    fs = p.fs;
+    f = p.f;
+    const int routed = n_ent - (fs > 0 ? 1 : 0);
+    split(fs + routed * f, c0, c1);  // at most 129 * 2^18 columns
+    split(p.d, o0, o1);
+    tiles = c1 > c0 ? (c1 + 15) / 16 - c0 / 16 : 0;
+    batches = (tiles + kFewBatch - 1) / kFewBatch;
+    groups = (o1 - o0 + kFewRowsW - 1) / kFewRowsW;
+    cd = p.d / CE;
+    cf = f / CE;
+    cs = fs / CE;
+    down_chunks = cs + routed * cf;
   }
-  __device__ __forceinline__ int width() const { return c.ent_e[ent] < 0 ? p.fs : p.f; }
-  __device__ __forceinline__ void settle() {  // phase 0: the tile at (ent, col), or on to phase 1
-    if (col >= c1) {
-      start_down();
-      return;
-    }
-    n = (int)min((int64_t)min(16, width() - col), c1 - col);
+  // this CTA's part of n columns: equal to one column
+  __device__ static __forceinline__ void split(int n, int& a, int& b) {
+    const int G = gridDim.x, i = blockIdx.x, each = n / G, rest = n - each * G;
+    a = each * i + min(i, rest);
+    b = a + each + (i < rest ? 1 : 0);
   }
-  __device__ __forceinline__ void start_down() {
-    phase = 1;
-    ent = 0;
-    col = (int)((int64_t)p.d * blockIdx.x / gridDim.x);
-    o1 = (int)((int64_t)p.d * (blockIdx.x + 1) / gridDim.x);
-    if (col >= o1 || c.n_ent == 0) phase = 2;
-    else n = min(kFewRowsW, o1 - col);
-  }
-  __device__ __forceinline__ void next() {
-    if (phase == 0) {
-      col += n;
-      if (col >= width() && c1 > width()) {
-        c1 -= width();
-        col = 0;
-        ++ent;
-      }
-      settle();
-    } else if (phase == 1) {
-      if (++ent == c.n_ent) {
-        ent = 0;
-        col += n;
-        if (col >= o1) {
-          phase = 2;
-          return;
-        }
-        n = min(kFewRowsW, o1 - col);
-      }
-    }
-  }
-  // the tile's inner dimension and this warp's share of it, in chunks of 64 bytes of a row
-  __device__ __forceinline__ int inner() const { return phase == 0 ? p.d : (c.ent_e[ent] < 0 ? p.fs : p.f); }
-  __device__ __forceinline__ void span(int warp, int& a, int& b) const {
-    const int chunks = inner() / (64 / (int)sizeof(T));
-    a = chunks * warp / kFewWarps;
-    b = chunks * (warp + 1) / kFewWarps;
+  __device__ __forceinline__ int batch_tiles(int s) const { return min(kFewBatch, tiles - s * kFewBatch); }
+  // chunks that warp w takes of the batch or group
+  __device__ __forceinline__ int begin(int phase, int s, int w) const {
+    return (phase == 0 ? batch_tiles(s) * cd : down_chunks) * w / kFewWarps;
   }
 };
 
-// The weight stream of one lane: 4 rows (q = 0..3) of the walk's current tile, 16 bytes per row
-// and chunk.  Gate/up: q & 1 picks W1 or W3, q >> 1 the upper 8 columns; down: 8 columns per q.
+// A run's part within one tile (gate/up) or entry (down).
+struct FewSeg {
+  int ent, chunk, left;
+  int tile;            // gate/up: its number in the batch
+  int col, lo, hi;     // gate/up: the tile's first column in the entry, and the columns [lo, hi) of it that are owned
+};
+template <typename T>
+__device__ __forceinline__ FewSeg few_segment(const FewShare<T>& h, int phase, int s, int pos, int end) {
+  FewSeg g;
+  const int shared = h.fs > 0 ? 1 : 0;
+  if (phase == 0) {
+    g.tile = pos / h.cd;
+    g.chunk = pos - g.tile * h.cd;
+    g.left = min(end - pos, h.cd - g.chunk);
+    const int gc = (h.c0 / 16 + s * kFewBatch + g.tile) * 16;
+    g.lo = max(0, h.c0 - gc);
+    g.hi = min(16, h.c1 - gc);
+    if (gc < h.fs) {
+      g.ent = 0;
+      g.col = gc;
+    } else {
+      const int r = gc - h.fs, i = r / h.f;
+      g.ent = shared + i;
+      g.col = r - i * h.f;
+    }
+  } else {
+    g.tile = g.col = g.lo = g.hi = 0;
+    if (pos < h.cs) {
+      g.ent = 0;
+      g.chunk = pos;
+      g.left = min(end, h.cs) - pos;
+    } else {
+      const int r = pos - h.cs, i = r / h.cf;
+      g.ent = shared + i;
+      g.chunk = r - i * h.cf;
+      g.left = min(end - pos, h.cf - g.chunk);
+    }
+  }
+  return g;
+}
+
+// The weight stream of one lane: 4 rows (q = 0..3) of the current tile, 16 bytes per row and chunk.
+// Gate/up: q & 1 picks W1 or W3, q >> 1 the upper 8 columns; down: 8 columns per q.
 template <typename T>
 struct FewStream {
-  FewWalk<T> walk;
+  const FewParams<T>& p;
+  const FewCtl& c;
+  const FewShare<T>& h;
   const T* ptr;
   int64_t s1, s2;  // offsets of q & 1 and q >> 1
   uint32_t live;   // q's whose row exists
-  int chunk, end;
+  int phase, s, pos, end, left;
   int warp, g, t;
 
-  __device__ FewStream(const FewParams<T>& p, const FewCtl& c, int warp_, int lane)
-      : walk(p, c), warp(warp_), g(lane >> 2), t(lane & 3) {
+  __device__ FewStream(const FewParams<T>& p_, const FewCtl& c_, const FewShare<T>& h_, int warp_, int lane)
+      : p(p_), c(c_), h(h_), phase(0), s(-1), pos(0), end(0), warp(warp_), g(lane >> 2), t(lane & 3) {
     open();
   }
-  __device__ __forceinline__ void open() {  // the first tile from here on in which this warp has chunks
-    while (walk.phase < 2) {
-      walk.span(warp, chunk, end);
-      if (chunk < end) break;
-      walk.next();
+  __device__ __forceinline__ void open() {  // the segment at pos, or the next batch or group with chunks for this warp
+    while (pos >= end) {
+      ++s;
+      if (phase == 0 && s >= h.batches) {
+        phase = 1;
+        s = 0;
+      }
+      if (phase == 1 && s >= h.groups) {
+        phase = 2;
+        return;
+      }
+      pos = h.begin(phase, s, warp);
+      end = h.begin(phase, s, warp + 1);
     }
-    if (walk.phase == 2) return;
-    const FewParams<T>& p = walk.p;
-    const int e = walk.c.ent_e[walk.ent];
+    const FewSeg sg = few_segment(h, phase, s, pos, end);
+    left = sg.left;
+    const int e = c.ent_e[sg.ent];
     const int64_t f = e < 0 ? p.fs : p.f, d = p.d;
     const T* base = e < 0 ? p.Ws : p.W + (int64_t)e * p.wstride;
     live = 0;
-    if (walk.phase == 0) {
-      ptr = base + (walk.col + g) * d;
+    if (phase == 0) {
+      ptr = base + (int64_t)(sg.col + g) * d;
       s1 = f * d;
       s2 = 8 * d;
-      live = (g < walk.n ? 3u : 0u) | (g + 8 < walk.n ? 12u : 0u);
+      live = (g >= sg.lo && g < sg.hi ? 3u : 0u) | (g + 8 >= sg.lo && g + 8 < sg.hi ? 12u : 0u);
     } else {
-      ptr = base + 2 * f * d + (walk.col + g) * f;
+      const int o = h.o0 + s * kFewRowsW;
+      ptr = base + 2 * f * d + (int64_t)(o + g) * f;
       s1 = 8 * f;
       s2 = 16 * f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) live |= (g + 8 * q < walk.n ? 1u : 0u) << q;
+      for (int q = 0; q < 4; ++q) live |= (o + g + 8 * q < h.o1 ? 1u : 0u) << q;
     }
-    ptr += (int64_t)chunk * (64 / sizeof(T)) + t * (16 / sizeof(T));
+    ptr += (int64_t)sg.chunk * (64 / sizeof(T)) + t * (16 / sizeof(T));
   }
-  // copies the next chunk into the stage (nothing once the walk has ended) and closes the group
+  // copies the next chunk into the stage (nothing once the share has ended) and closes the group
   __device__ __forceinline__ void issue(uint32_t dst) {
-    if (walk.phase < 2) {
+    if (phase < 2) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (live >> q & 1u) cp_async16(dst + q * 512, ptr + (q & 1) * s1 + (q >> 1) * s2);
       ptr += 64 / sizeof(T);
-      if (++chunk == end) {
-        walk.next();
-        open();
-      }
+      ++pos;
+      if (--left == 0) open();
     }
     cp_async_commit();
   }
@@ -232,120 +261,262 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   return v;
 }
 
-// One tile of one warp: its partial sums [32 weight rows][ntok] into red.  rows: the token operand's
-// rows (x by token in phase 0, H by row in phase 1), this lane's 16 bytes at chunk `a`.
+// Sums of one lane over chunks: bf16 [2 blocks of 16 weight rows][NT blocks of 8 columns][4], in the
+// instruction's layout; fp32 [4 rows][8 NT columns], this lane's part of each chunk.
 template <typename T, int NT>
-__device__ __forceinline__ void few_tile(FewStream<T>& st, uint32_t ring, int& slot, int a, int b, bool down,
-                                         const T* rows, int64_t ld, const uint8_t* tok, int ntok, float* red, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  constexpr int CE = 64 / sizeof(T);  // elements of a chunk
-  if constexpr (sizeof(T) == 2) {
-    float acc[2][NT][4] = {};
-    const T* src[NT];
-    bool has[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      has[j] = g + 8 * j < ntok;
-      const int r = has[j] ? (tok ? tok[g + 8 * j] : g + 8 * j) : 0;
-      src[j] = rows + r * ld + (int64_t)a * CE + t * 8;
-    }
-    for (int ch = a; ch < b; ++ch) {
-      uint4 xb[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        xb[j] = make_uint4(0, 0, 0, 0);
-        if (has[j]) xb[j] = down ? __ldcg(reinterpret_cast<const uint4*>(src[j])) : __ldg(reinterpret_cast<const uint4*>(src[j]));
-        src[j] += CE;
-      }
-      cp_async_wait<kFewDepth - 1>();
-      uint4 wq[4];
-      const uint32_t at = ring + slot * kFewStage;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) wq[q] = lds16(at + q * 512);
-      slot = slot + 1 == kFewDepth ? 0 : slot + 1;
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma_bf16(acc[m][j], wq[2 * m].x, wq[2 * m + 1].x, wq[2 * m].y, wq[2 * m + 1].y, xb[j].x, xb[j].y);
-          mma_bf16(acc[m][j], wq[2 * m].z, wq[2 * m + 1].z, wq[2 * m].w, wq[2 * m + 1].w, xb[j].z, xb[j].w);
-        }
-      st.issue(at);  // the stage's values have been used: it may be filled again
-    }
-    // row q * 8 + g of the tile, token columns 8 j + 2 t and the next
+struct FewAcc;
+template <int NT>
+struct FewAcc<__nv_bfloat16, NT> {
+  float v[2][NT][4];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(red + ((2 * m + h) * 8 + g) * kFewPitch + 8 * j + 2 * t) =
-              make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-  } else {
-    float acc[4][8 * NT];
+        for (int i = 0; i < 4; ++i) v[m][j][i] = 0.f;
+  }
+  // row q * 8 + g of the tile, token columns 8 j + 2 t and the next
+  __device__ __forceinline__ void store(float* red, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<float2*>(red + ((2 * m + i) * 8 + g) * kFewPitch + 8 * j + 2 * t) =
+              make_float2(v[m][j][2 * i], v[m][j][2 * i + 1]);
+  }
+};
+template <int NT>
+struct FewAcc<float, NT> {
+  float v[4][8 * NT];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int j = 0; j < 8 * NT; ++j) acc[q][j] = 0.f;
-    for (int ch = a; ch < b; ++ch) {
+      for (int j = 0; j < 8 * NT; ++j) v[q][j] = 0.f;
+  }
+  __device__ __forceinline__ void store(float* red, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < 8 * NT; ++j) {
+        v[q][j] += __shfl_xor_sync(0xffffffffu, v[q][j], 1);
+        v[q][j] += __shfl_xor_sync(0xffffffffu, v[q][j], 2);
+        if ((j & 3) == t) red[(q * 8 + g) * kFewPitch + j] = v[q][j];
+      }
+  }
+};
+
+// `n` chunks of the stream times the columns' rows.  Column j of `cols` has its row at row(j) elements
+// behind `rows` (row(j) < 0: the column is zero); `at`: the first chunk's element.  kH: the rows were
+// written by this launch (read them from L2); scale(j) multiplies the column's values (fp32 only).
+template <typename T, int NT, bool kH, typename Row, typename Scale>
+__device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int& slot, int n, const T* rows, int at,
+                                           Row row, Scale scale, FewAcc<T, NT>& acc, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  constexpr int CE = 64 / sizeof(T);
+  auto load = [](const T* s) {
+    return kH ? __ldcg(reinterpret_cast<const uint4*>(s)) : __ldg(reinterpret_cast<const uint4*>(s));
+  };
+  if constexpr (sizeof(T) == 2) {
+    const T* src[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int64_t r = row(g + 8 * j);
+      src[j] = r < 0 ? nullptr : rows + r + at + t * 8;
+    }
+    // the token operand of the next chunk is loaded while this one is multiplied
+    uint4 xn[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      xn[j] = make_uint4(0, 0, 0, 0);
+      if (src[j]) xn[j] = load(src[j]);
+    }
+    for (int i = 0; i < n; ++i) {
+      uint4 xb[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        xb[j] = xn[j];
+        if (src[j] && i + 1 < n) xn[j] = load(src[j] + (i + 1) * CE);
+      }
       cp_async_wait<kFewDepth - 1>();
       uint4 wq[4];
-      const uint32_t at = ring + slot * kFewStage;
+      const uint32_t from = ring + slot * kFewStage;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) wq[q] = lds16(at + q * 512);
+      for (int q = 0; q < 4; ++q) wq[q] = lds16(from + q * 512);
+      slot = slot + 1 == kFewDepth ? 0 : slot + 1;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_bf16(acc.v[m][j], wq[2 * m].x, wq[2 * m + 1].x, wq[2 * m].y, wq[2 * m + 1].y, xb[j].x, xb[j].y);
+          mma_bf16(acc.v[m][j], wq[2 * m].z, wq[2 * m + 1].z, wq[2 * m].w, wq[2 * m + 1].w, xb[j].z, xb[j].w);
+        }
+      st.issue(from);  // the stage's values have been used: it may be filled again
+    }
+  } else {
+    for (int i = 0; i < n; ++i) {
+      cp_async_wait<kFewDepth - 1>();
+      uint4 wq[4];
+      const uint32_t from = ring + slot * kFewStage;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) wq[q] = lds16(from + q * 512);
       slot = slot + 1 == kFewDepth ? 0 : slot + 1;
 #pragma unroll
       for (int j = 0; j < 8 * NT; ++j) {
-        if (j < ntok) {
-          const uint4* src = reinterpret_cast<const uint4*>(rows + (tok ? tok[j] : j) * ld + (int64_t)ch * CE + t * 4);
-          const uint4 xb = down ? __ldcg(src) : __ldg(src);
+        const int64_t r = row(j);
+        if (r >= 0) {
+          uint4 xb = load(rows + r + at + i * CE + t * 4);
+          if (kH) {
+            const float sc = scale(j);
+            xb.x = __float_as_uint(__uint_as_float(xb.x) * sc);
+            xb.y = __float_as_uint(__uint_as_float(xb.y) * sc);
+            xb.z = __float_as_uint(__uint_as_float(xb.z) * sc);
+            xb.w = __float_as_uint(__uint_as_float(xb.w) * sc);
+          }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[q][j] = dot16(xb, wq[q], acc[q][j], (const float*)nullptr);
+          for (int q = 0; q < 4; ++q) acc.v[q][j] = dot16(xb, wq[q], acc.v[q][j], (const float*)nullptr);
         }
       }
-      st.issue(at);  // the stage's values have been used: it may be filled again
+      st.issue(from);  // the stage's values have been used: it may be filled again
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int j = 0; j < 8 * NT; ++j) {
-        acc[q][j] += __shfl_xor_sync(0xffffffffu, acc[q][j], 1);
-        acc[q][j] += __shfl_xor_sync(0xffffffffu, acc[q][j], 2);
-        if ((j & 3) == t) red[(q * 8 + g) * kFewPitch + j] = acc[q][j];
-      }
   }
 }
 
+// Gate/up of one segment: partial sums [32 weight rows][tokens of the entry] into red.
+template <typename T, int NT>
+__device__ __forceinline__ void few_gate_up(FewStream<T>& st, uint32_t ring, int& slot, const FewSeg& sg, const T* x,
+                                            int d, const uint8_t* tok, int ntok, float* red, int lane) {
+  FewAcc<T, NT> acc;
+  acc.clear();
+  few_chunks<T, NT, false>(
+      st, ring, slot, sg.left, x, sg.chunk * (64 / (int)sizeof(T)),
+      [&](int j) { return j < ntok ? (int64_t)tok[j] * d : (int64_t)-1; }, [](int) { return 1.f; }, acc, lane);
+  acc.store(red, lane);
+}
+
+// Down of one group of 32 output columns: this warp's run over all entries, partial sums
+// [32 columns][tokens] of the weighted sum into red.
+template <typename T, int NT>
+__device__ __forceinline__ void few_down(FewStream<T>& st, uint32_t ring, int& slot, const FewParams<T>& p,
+                                         const FewCtl& c, const FewShare<T>& h, int s, int warp, float* red, int lane) {
+  FewAcc<T, NT> sum;
+  sum.clear();
+  const int end = h.begin(1, s, warp + 1);
+  for (int pos = h.begin(1, s, warp); pos < end;) {
+    const FewSeg sg = few_segment(h, 1, s, pos, end);
+    const bool shared = c.ent_e[sg.ent] < 0;
+    const int f = shared ? p.fs : p.f;
+    const T* H = (shared ? p.Hs : p.H) + (int64_t)c.ent_row[sg.ent] * f;
+    const uint32_t mask = c.ent_mask[sg.ent];
+    const float* wt = c.ent_w[sg.ent];
+    auto row = [&](int j) { return mask >> j & 1u ? (int64_t)__popc(mask & ((1u << j) - 1u)) * f : (int64_t)-1; };
+    auto scale = [&](int j) { return wt[j]; };
+    const int at = sg.chunk * (64 / (int)sizeof(T));
+    if constexpr (sizeof(T) == 2) {
+      FewAcc<T, NT> acc;
+      acc.clear();
+      few_chunks<T, NT, true>(st, ring, slot, sg.left, H, at, row, scale, acc, lane);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int col = 8 * j + 2 * (lane & 3) + b;
+          if (mask >> col & 1u) {
+            const float w = wt[col];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              sum.v[m][j][b] = fmaf(w, acc.v[m][j][b], sum.v[m][j][b]);
+              sum.v[m][j][2 + b] = fmaf(w, acc.v[m][j][2 + b], sum.v[m][j][2 + b]);
+            }
+          }
+        }
+    } else {
+      few_chunks<T, NT, true>(st, ring, slot, sg.left, H, at, row, scale, sum, lane);
+    }
+    pos += sg.left;
+  }
+  sum.store(red, lane);
+}
+
+// Logits: one task per (expert, tg tokens); a CTA's threads split d.
 template <typename T>
 __device__ __forceinline__ void few_router(const FewParams<T>& p, FewCtl& c) {
   constexpr int V = 16 / sizeof(T);
+  constexpr int B = 4;  // token rows whose loads are in flight together
   const int nvec = p.d / V, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = blockIdx.x; e < p.E; e += gridDim.x) {
-    float acc[kFewMaxT];
-#pragma unroll
-    for (int t = 0; t < kFewMaxT; ++t) acc[t] = 0.f;
+  const int ntg = (p.T_ + p.tg - 1) / p.tg;
+  for (int task = blockIdx.x; task < p.E * ntg; task += gridDim.x) {
+    const int e = task / ntg, t0 = (task - e * ntg) * p.tg, nt = min(p.tg, p.T_ - t0);
     const uint4* wr = reinterpret_cast<const uint4*>(p.router_w + (int64_t)e * p.d);
-    for (int v = threadIdx.x; v < nvec; v += kFewThreads) {
-      const uint4 w = __ldg(wr + v);
+    for (int tb = 0; tb < nt; tb += B) {
+      const uint4* xr = reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + tb) * p.d);
+      float acc[B] = {0.f, 0.f, 0.f, 0.f};
+      for (int v = threadIdx.x; v < nvec; v += kFewThreads) {
+        const uint4 w = __ldg(wr + v);
+        uint4 x[B];
 #pragma unroll
-      for (int t = 0; t < kFewMaxT; ++t)
-        if (t < p.T_) acc[t] = dot16(__ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.d) + v), w, acc[t], p.x);
-    }
+        for (int i = 0; i < B; ++i) x[i] = __ldg(xr + (int64_t)(tb + i < nt ? i : 0) * nvec + v);
 #pragma unroll
-    for (int t = 0; t < kFewMaxT; ++t) {
-      if (t >= p.T_) break;
+        for (int i = 0; i < B; ++i) acc[i] = dot16(x[i], w, acc[i], p.x);
+      }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-      if (lane == 0) c.part[warp][t] = acc[t];
+      for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < B; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+      if (lane < B && tb + lane < nt) c.part[warp][tb + lane] = lane == 0 ? acc[0] : lane == 1 ? acc[1] : lane == 2 ? acc[2] : acc[3];
     }
     __syncthreads();
-    if (threadIdx.x < p.T_) {
+    if (threadIdx.x < nt) {
       float s = 0.f;
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) s += c.part[w][threadIdx.x];
-      p.logits[(int64_t)threadIdx.x * p.E + e] = s + (p.router_b ? __ldg(p.router_b + e) : 0.f);
+      p.logits[(int64_t)(t0 + threadIdx.x) * p.E + e] = s + (p.router_b ? __ldg(p.router_b + e) : 0.f);
     }
     __syncthreads();
+  }
+}
+
+// One warp selects the top-k of one token from its E logits in shared memory (which it overwrites):
+// the largest value first, lower index on ties.  The values are compared as integers in their order
+// (adding zero makes -0 and 0 the same value), so that a step is two warp reductions.
+__device__ __forceinline__ void few_topk(float* lg, int E, int k, int flags, int lane, int32_t* idx, float* w) {
+  uint32_t* key = reinterpret_cast<uint32_t*>(lg);
+  for (int e = lane; e < E; e += 32) {
+    const uint32_t b = __float_as_uint(router_clamp(lg[e], flags) + 0.f);
+    key[e] = max(1u, b & 0x80000000u ? ~b : b | 0x80000000u);  // 0: chosen already
+  }
+  float den = 0.f, first = 0.f, mine = 0.f;
+  int at = 0;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0;
+    int e_best = 0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32)
+      if (key[e] > best) {
+        best = key[e];
+        e_best = e;
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)e_best : 0xffffffffu);
+    if ((e & 31) == lane) key[e] = 0u;
+    const float v = __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
+    if (j == 0) first = v;
+    const float p = (flags & kRouterRaw) ? v : expf(v - first);
+    den += p;
+    if (lane == j) {
+      mine = p;
+      at = e;
+    }
+  }
+  if (lane < k) {
+    idx[lane] = at;
+    w[lane] = (flags & kRouterRaw) ? mine : mine / den;
   }
 }
 
@@ -358,7 +529,7 @@ __device__ __forceinline__ void few_select(const FewParams<T>& p, FewCtl& c, flo
   for (int e = threadIdx.x; e < E; e += kFewThreads) c.mask[e] = 0;
   __syncthreads();
   if (warp < T_) {
-    warp_topk(lg + warp * E, E, k, p.flags, lane, c.idx + warp * k, c.w + warp * k);
+    few_topk(lg + warp * E, E, k, p.flags, lane, c.idx + warp * k, c.w + warp * k);
     __syncwarp();
     if (lane < k) {
       const int e = min(max(c.idx[warp * k + lane], 0), E - 1);
@@ -373,8 +544,12 @@ __device__ __forceinline__ void few_select(const FewParams<T>& p, FewCtl& c, flo
       c.ent_e[0] = -1;
       c.ent_row[0] = 0;
       c.ent_n[0] = T_;
+      c.ent_mask[0] = (1u << T_) - 1u;
     }
-    if (n && lane < kFewMaxT) c.ent_tok[0][lane] = (uint8_t)lane;
+    if (n && lane < kFewMaxT) {
+      c.ent_tok[0][lane] = (uint8_t)lane;
+      c.ent_w[0][lane] = 1.f;
+    }
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
       const uint32_t m = e < E ? c.mask[e] : 0u;
@@ -392,6 +567,8 @@ __device__ __forceinline__ void few_select(const FewParams<T>& p, FewCtl& c, flo
         c.ent_e[i] = e;
         c.ent_row[i] = row + incl - cnt;
         c.ent_n[i] = cnt;
+        c.ent_mask[i] = m;
+        c.mask[e] = m | (uint32_t)i << 16;  // the entry beside the tokens
         uint32_t left = m;
         for (int j = 0; left; ++j, left &= left - 1) c.ent_tok[i][j] = (uint8_t)(__ffs(left) - 1);
       }
@@ -404,10 +581,11 @@ __device__ __forceinline__ void few_select(const FewParams<T>& p, FewCtl& c, flo
     }
   }
   __syncthreads();
+  if (threadIdx.x < T_ * k) c.ent_w[c.mask[c.idx[threadIdx.x]] >> 16][threadIdx.x / k] = c.w[threadIdx.x];
   if (blockIdx.x == 0) {
     for (int e = threadIdx.x; e <= E; e += kFewThreads) {
       p.offsets[e] = c.off[e];
-      if (e < E) p.counts[e] = __popc(c.mask[e]);
+      if (e < E) p.counts[e] = __popc(c.mask[e] & 0xffffu);
     }
     for (int i = threadIdx.x; i < T_ * k; i += kFewThreads) {
       const int t = i / k, e = c.idx[i], r = c.off[e] + __popc(c.mask[e] & ((1u << t) - 1u));
@@ -425,7 +603,7 @@ __device__ __forceinline__ bool few_barrier(const FewParams<T>& p, FewCtl& c, in
   __syncthreads();
   if (threadIdx.x == 0) {
     const bool was = c.ok != 0;
-    const bool got = grid_sync(p.bar + i, gridDim.x, &c.abort);
+    const bool got = grid_sync<0>(p.bar + i, gridDim.x, &c.abort);
     if (!got) {
       c.abort = 1;
       atomicOr(p.err, kErrWaitTimeout);
@@ -439,8 +617,8 @@ __device__ __forceinline__ bool few_barrier(const FewParams<T>& p, FewCtl& c, in
 template <typename T>
 __global__ void __launch_bounds__(kFewThreads, 1) few_tokens_kernel(const __grid_constant__ FewParams<T> p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  float* red0 = reinterpret_cast<float*>(smem + kFewRing);
-  FewCtl& c = *reinterpret_cast<FewCtl*>(smem + kFewRing + 2 * kFewRed);
+  float* red = reinterpret_cast<float*>(smem + kFewRing);
+  FewCtl& c = *reinterpret_cast<FewCtl*>(smem + kFewRing + kFewRed);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     c.abort = 0;
@@ -451,70 +629,64 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_tokens_kernel(const __grid
     few_barrier(p, c, 1);
     return;
   }
-  few_select(p, c, red0);
+  few_select(p, c, red);
   __syncthreads();
 
+  const FewShare<T> h(p, c.n_ent);
   const uint32_t ring = smem_u32(smem) + warp * (kFewDepth * kFewStage) + lane * 16;
-  FewStream<T> st(p, c, warp, lane);
+  FewStream<T> st(p, c, h, warp, lane);
   for (int s = 0; s < kFewDepth; ++s) st.issue(ring + s * kFewStage);
-  int slot = 0, buf = 0, phase = 0;
-  for (FewWalk<T> w(p, c);; w.next()) {
-    if (w.phase != phase && phase == 0) {
-      // H of every CTA is written; the copies of the first W2 chunks are already in flight
-      phase = 1;
-      if (!few_barrier(p, c, 1)) break;
+  int slot = 0;
+
+  for (int s = 0; s < h.batches; ++s) {
+    const int end = h.begin(0, s, warp + 1);
+    for (int pos = h.begin(0, s, warp); pos < end;) {
+      const FewSeg sg = few_segment(h, 0, s, pos, end);
+      const int ntok = c.ent_n[sg.ent];
+      float* mine = red + (sg.tile + warp) * kFewSlot;
+      if (ntok <= 8) few_gate_up<T, 1>(st, ring, slot, sg, p.x, p.d, c.ent_tok[sg.ent], ntok, mine, lane);
+      else few_gate_up<T, 2>(st, ring, slot, sg, p.x, p.d, c.ent_tok[sg.ent], ntok, mine, lane);
+      pos += sg.left;
     }
-    if (w.phase == 2) break;
-    const bool down = phase == 1;
-    const int e = c.ent_e[w.ent], ntok = c.ent_n[w.ent], row0 = c.ent_row[w.ent];
-    const uint8_t* tok = c.ent_tok[w.ent];
-    const int f = e < 0 ? p.fs : p.f;
-    T* H = (e < 0 ? p.Hs : p.H) + (int64_t)row0 * f;
-    if (down && w.ent == 0) c.yacc[threadIdx.x >> 5][lane] = 0.f;
-    float* red = red0 + buf * (kFewRed / 4);
-    float* mine = red + warp * (kFewRowsW * kFewPitch);
-    int a, b;
-    w.span(warp, a, b);
-    const T* rows = down ? H : p.x;
-    const int64_t ld = down ? f : p.d;
-    if (ntok <= 8) few_tile<T, 1>(st, ring, slot, a, b, down, rows, ld, down ? nullptr : tok, ntok, mine, lane);
-    else few_tile<T, 2>(st, ring, slot, a, b, down, rows, ld, down ? nullptr : tok, ntok, mine, lane);
     __syncthreads();
-    if (!down) {
-      const int col = threadIdx.x & 15, n = threadIdx.x >> 4;
-      if (n < ntok && col < w.n) {
-        const int r = (col >> 3) * 16 + (col & 7);
-        float gt = 0.f, up = 0.f;
-#pragma unroll
-        for (int i = 0; i < kFewWarps; ++i) {
-          gt += red[(i * kFewRowsW + r) * kFewPitch + n];
-          up += red[(i * kFewRowsW + r + 8) * kFewPitch + n];
+    // h = silu(g) * u: a thread per column of the batch's tiles, and token
+    const int nt = h.batch_tiles(s), all = nt * h.cd;
+    for (int i = threadIdx.x; i < nt * 256; i += kFewThreads) {
+      const int tile = i >> 8, col = i & 15, n = (i >> 4) & 15;
+      const FewSeg sg = few_segment(h, 0, s, tile * h.cd, all);
+      if (n >= c.ent_n[sg.ent] || col < sg.lo || col >= sg.hi) continue;
+      const int r = (col >> 3) * 16 + (col & 7);
+      float gt = 0.f, up = 0.f;
+      for (int w = 0; w < kFewWarps; ++w) {
+        const int a = all * w / kFewWarps, b = all * (w + 1) / kFewWarps;
+        if (max(a, tile * h.cd) < min(b, (tile + 1) * h.cd)) {
+          const float* v = red + (tile + w) * kFewSlot + r * kFewPitch + n;
+          gt += v[0];
+          up += v[8 * kFewPitch];
         }
-        H[(int64_t)n * f + w.col + col] = from_f32<T>(silu_mul(gt, up));
       }
-    } else {
-      const int n = warp;
-      if (n < ntok && lane < w.n) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < kFewWarps; ++i) v += red[(i * kFewRowsW + lane) * kFewPitch + n];
-        const int t = tok[n];
-        float wt = 1.f;
-        if (e >= 0) {
-          for (int j = 0; j < p.k; ++j)
-            if (c.idx[t * p.k + j] == e) {
-              wt = c.w[t * p.k + j];
-              break;
-            }
-        }
-        c.yacc[t][lane] = fmaf(wt, v, c.yacc[t][lane]);
-      }
-      if (w.ent == c.n_ent - 1) {
-        __syncthreads();
-        if (warp < p.T_ && lane < w.n) p.y[(int64_t)warp * p.d + w.col + lane] = from_f32<T>(c.yacc[warp][lane]);
-      }
+      const bool shared = c.ent_e[sg.ent] < 0;
+      const int f = shared ? p.fs : p.f;
+      T* H = (shared ? p.Hs : p.H) + (int64_t)(c.ent_row[sg.ent] + n) * f;
+      H[sg.col + col] = from_f32<T>(silu_mul(gt, up));
     }
-    buf ^= 1;
+    __syncthreads();
+  }
+
+  // H of every CTA is written; the copies of the first W2 chunks are already in flight
+  const bool ok = few_barrier(p, c, 1);
+  for (int s = 0; ok && s < h.groups; ++s) {
+    if (p.T_ <= 8) few_down<T, 1>(st, ring, slot, p, c, h, s, warp, red + warp * kFewSlot, lane);
+    else few_down<T, 2>(st, ring, slot, p, c, h, s, warp, red + warp * kFewSlot, lane);
+    __syncthreads();
+    const int o = h.o0 + s * kFewRowsW + lane;
+    if (warp < p.T_ && o < h.o1) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) v += red[w * kFewSlot + lane * kFewPitch + warp];
+      p.y[(int64_t)warp * p.d + o] = from_f32<T>(v);
+    }
+    __syncthreads();
   }
   cp_async_wait<0>();
 }
@@ -547,6 +719,9 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t s) {
   p.E = a.E;
   p.k = a.k;
   p.flags = a.router_flags;
+  // as few tokens per task as lets all tasks run at once
+  const int groups = a.sm_count / a.E < 1 ? 1 : (a.sm_count / a.E < a.T ? a.sm_count / a.E : a.T);
+  p.tg = (a.T + groups - 1) / groups;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.sm_count);
   cfg.blockDim = dim3(kFewThreads);

@@ -120,6 +120,7 @@ class Case:
         err += HALF[self.dt] * (ref.abs() + err)
         bad = ~((y.double() - ref).abs() <= err + 1e-37)
         assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}"
+        return err
 
 
 @pytest.mark.gpu
@@ -173,13 +174,18 @@ def test_decode_ties_go_to_the_lower_index(dt):
 def test_decode_values_that_are_not_finite_stay_in_their_token(dt):
     c = Case(4, 256, 128, 4, 2, 0, dt)
     clean = c.decode().clone()
+    err = c.check(clean)
     c.x[1, 3] = float("nan")
     c.x[2, 7] = float("inf")
     y = c.decode()
     torch.cuda.synchronize()
     c.layer.sync_status()
     assert torch.isnan(y[1]).all() and not torch.isfinite(y[2]).any()
-    assert torch.equal(y[0], clean[0]) and torch.equal(y[3], clean[3])
+    # The other tokens: where a warp's run of a sum ends depends on which experts the batch touches, and
+    # tokens 1 and 2 may now choose others, so the sums may be grouped differently; both results are
+    # within `err` of the same exact value, so they are within twice that of each other.
+    for t in (0, 3):
+        assert ((y[t].double() - clean[t].double()).abs() <= 2 * err[t]).all()
 
 
 @pytest.mark.gpu
