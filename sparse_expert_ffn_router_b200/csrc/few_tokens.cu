@@ -322,33 +322,36 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
   auto load = [](const T* s) {
     return kH ? __ldcg(reinterpret_cast<const uint4*>(s)) : __ldg(reinterpret_cast<const uint4*>(s));
   };
-  if constexpr (sizeof(T) == 2) {
-    const T* src[NT];
+  const T* src[NT];
+  float sc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t r = row(g + 8 * j);
+    src[j] = r < 0 ? nullptr : rows + r + at + t * (16 / (int)sizeof(T));
+    sc[j] = kH && r >= 0 ? scale(g + 8 * j) : 1.f;
+  }
+  // a lane holds 16 bytes of the columns g and g + 8; those of the next chunk are loaded while this
+  // one is multiplied
+  uint4 xn[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    xn[j] = make_uint4(0, 0, 0, 0);
+    if (src[j]) xn[j] = load(src[j]);
+  }
+  for (int i = 0; i < n; ++i) {
+    uint4 xb[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int64_t r = row(g + 8 * j);
-      src[j] = r < 0 ? nullptr : rows + r + at + t * 8;
+      xb[j] = xn[j];
+      if (src[j] && i + 1 < n) xn[j] = load(src[j] + (i + 1) * CE);
     }
-    // the token operand of the next chunk is loaded while this one is multiplied
-    uint4 xn[NT];
+    cp_async_wait<kFewDepth - 1>();
+    uint4 wq[4];
+    const uint32_t from = ring + slot * kFewStage;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      xn[j] = make_uint4(0, 0, 0, 0);
-      if (src[j]) xn[j] = load(src[j]);
-    }
-    for (int i = 0; i < n; ++i) {
-      uint4 xb[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        xb[j] = xn[j];
-        if (src[j] && i + 1 < n) xn[j] = load(src[j] + (i + 1) * CE);
-      }
-      cp_async_wait<kFewDepth - 1>();
-      uint4 wq[4];
-      const uint32_t from = ring + slot * kFewStage;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) wq[q] = lds16(from + q * 512);
-      slot = slot + 1 == kFewDepth ? 0 : slot + 1;
+    for (int q = 0; q < 4; ++q) wq[q] = lds16(from + q * 512);
+    slot = slot + 1 == kFewDepth ? 0 : slot + 1;
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -356,34 +359,26 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
           mma_bf16(acc.v[m][j], wq[2 * m].x, wq[2 * m + 1].x, wq[2 * m].y, wq[2 * m + 1].y, xb[j].x, xb[j].y);
           mma_bf16(acc.v[m][j], wq[2 * m].z, wq[2 * m + 1].z, wq[2 * m].w, wq[2 * m + 1].w, xb[j].z, xb[j].w);
         }
-      st.issue(from);  // the stage's values have been used: it may be filled again
-    }
-  } else {
-    for (int i = 0; i < n; ++i) {
-      cp_async_wait<kFewDepth - 1>();
-      uint4 wq[4];
-      const uint32_t from = ring + slot * kFewStage;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) wq[q] = lds16(from + q * 512);
-      slot = slot + 1 == kFewDepth ? 0 : slot + 1;
+    } else {
+      // every lane needs every column's bytes: they come from the lane that loaded them
 #pragma unroll
       for (int j = 0; j < 8 * NT; ++j) {
-        const int64_t r = row(j);
-        if (r >= 0) {
-          uint4 xb = load(rows + r + at + i * CE + t * 4);
-          if (kH) {
-            const float sc = scale(j);
-            xb.x = __float_as_uint(__uint_as_float(xb.x) * sc);
-            xb.y = __float_as_uint(__uint_as_float(xb.y) * sc);
-            xb.z = __float_as_uint(__uint_as_float(xb.z) * sc);
-            xb.w = __float_as_uint(__uint_as_float(xb.w) * sc);
-          }
+        if (row(j) < 0) continue;
+        const uint4& x = xb[j >> 3];
+        const float s = sc[j >> 3];
+        float xs[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc.v[q][j] = dot16(xb, wq[q], acc.v[q][j], (const float*)nullptr);
+        for (int k = 0; k < 4; ++k) xs[k] = __shfl_sync(0xffffffffu, kH ? xs[k] * s : xs[k], (j & 7) * 4 + t);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          acc.v[q][j] = fmaf(xs[0], __uint_as_float(wq[q].x), acc.v[q][j]);
+          acc.v[q][j] = fmaf(xs[1], __uint_as_float(wq[q].y), acc.v[q][j]);
+          acc.v[q][j] = fmaf(xs[2], __uint_as_float(wq[q].z), acc.v[q][j]);
+          acc.v[q][j] = fmaf(xs[3], __uint_as_float(wq[q].w), acc.v[q][j]);
         }
       }
-      st.issue(from);  // the stage's values have been used: it may be filled again
     }
+    st.issue(from);  // the stage's values have been used: it may be filled again
   }
 }
 
