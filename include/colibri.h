@@ -254,7 +254,9 @@ colibri_status colibri_combine(const void* Yp, int32_t act_dtype, const int32_t*
  * `stream`; calls may overlap on the GPU.  Row strides (ld*) are in elements; the rows of x, q, A
  * and W must start on 16-byte boundaries, those of y need not.  K (cols) is a multiple of 16, up
  * to 131056 (the int32 sums are exact); N up to 2^20, rows up to 2^24; zero rows launch nothing.
- * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA; reason via colibri_last_error(NULL).
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA; reason via colibri_last_error(NULL).  A
+ * device-side wait that gives up is reported by colibri_int_check.  The first call on each device
+ * loads the kernels and should come before any stream capture.
  *
  * colibri_quantize_rows -- per row r of x [rows, cols] (act_dtype F32 or BF16):
  *   scale[r] = max |x[r][:]| / 127 in fp32; q[r][c] = the integer nearest to the exact quotient
@@ -302,6 +304,14 @@ colibri_status colibri_int_swiglu_experts(const int8_t* A, int64_t lda, const fl
                                           const float* w_scale, int64_t s_stride, int32_t N,
                                           int32_t K, void* h, int64_t ldh, int32_t out_dtype,
                                           void* stream);
+
+/*
+ * colibri_int_check -- synchronise `stream` and report whether a bounded device wait of an int8
+ * product called since the last check on the current device gave up (COLIBRI_ERR_TIMEOUT; that
+ * product's output is then undefined).  One word per device, shared by all streams, cleared by the
+ * check.  Blocking.  Errors: TIMEOUT, CUDA.
+ */
+colibri_status colibri_int_check(void* stream);
 
 /*
  * colibri_sync_status -- synchronise `stream`, then read and clear the context's device

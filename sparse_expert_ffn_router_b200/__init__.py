@@ -43,6 +43,7 @@ EXPORTS = (
     "colibri_int_gemm",
     "colibri_int_gemm_experts",
     "colibri_int_swiglu_experts",
+    "colibri_int_check",
     "colibri_sync_status",
     "colibri_profile_begin",
     "colibri_profile_end",
@@ -112,6 +113,8 @@ def load() -> ctypes.CDLL:
     for f in (lib.colibri_int_gemm_experts, lib.colibri_int_swiglu_experts):
         f.argtypes = [vp, i64, vp, i32, vp, i32, vp, i64, vp, i64, i32, i32, vp, i64, i32, vp]
         f.restype = ctypes.c_int
+    lib.colibri_int_check.argtypes = [vp]
+    lib.colibri_int_check.restype = ctypes.c_int
     lib.colibri_sync_status.argtypes = [vp, vp]
     lib.colibri_sync_status.restype = ctypes.c_int
     lib.colibri_profile_begin.argtypes = [vp, i32]
@@ -242,6 +245,11 @@ def colibri_int_swiglu_experts(A, lda: int, a_scale, rows: int, offsets, num_exp
     _check(load().colibri_int_swiglu_experts(_addr(A), lda, _addr(a_scale), rows, _addr(offsets), num_experts,
                                              _addr(W), w_stride, _addr(w_scale), s_stride, N, K, _addr(h), ldh,
                                              out_dtype, _stream(stream)), "colibri_int_swiglu_experts")
+
+
+def colibri_int_check(stream=None) -> None:
+    """Raises ColibriError(TIMEOUT) if a device wait of an int8 product gave up since the last check."""
+    _check(load().colibri_int_check(_stream(stream)), "colibri_int_check")
 
 
 def colibri_sync_status(ctx: int, stream=None) -> None:

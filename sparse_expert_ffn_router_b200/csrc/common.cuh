@@ -403,7 +403,9 @@ struct IntGemmArgs {
   void* y;                 // [rows, N], row stride ldy
   int64_t ldy;
   int out_dtype;           // COLIBRI_F32 or COLIBRI_BF16
+  uint32_t* err;           // error word of bounded waits, or nullptr: the library's own word per device
 };
+cudaError_t int_gemm_take_error(uint32_t* word);  // reads and clears the current device's own word
 cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s);
 cudaError_t launch_quantize_rows(const void* x, int act, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,
                                  float* scale, cudaStream_t s);

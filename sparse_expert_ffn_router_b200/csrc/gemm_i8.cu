@@ -6,112 +6,587 @@
 // The rows may be grouped: rows [offsets[e], offsets[e+1]) meet the weights of expert e.  The sums
 // over k are exact int32 (K <= 131056, so that K * 128 * 128 stays below 2^31); the conversion to
 // fp32 and the two scales round once each, and the result once to its type.
+//
+// i8_pair_kernel: clusters of two CTAs (tcgen05 cta_group::2, kind::i8), persistent, one pair per two
+// SMs, 192 threads per CTA:
+//   warp 0      TMA producer: this CTA's 128 rows of A and 128 of the 256 weight rows of the tile
+//               (SwiGLU: the leader W1, the peer W3), 128 bytes of k per stage, into a ring of 32 KB
+//               stages; both CTAs' copies count on the leader's barrier.
+//   warp 1      the leader issues the M = 256, N = 256, K = 32 MMAs, four per stage, into one of two
+//               accumulators (128 rows x 256 int32 columns of TMEM in each CTA).
+//   warps 2-5   epilogue: TMEM -> registers, scales, SwiGLU, stores; it overlaps the next tile's MMAs.
+// A group's last m-tile of at most 128 rows runs with the operands swapped (weights the M side, its
+// rows rounded up to 32 the N side), so that a group of a few rows costs the stream of its weights
+// and little else; with at most 32 rows a stage holds two k blocks of weights.  For SwiGLU a swapped
+// tile's 128 weight rows per CTA are 4 x (16 of W1, the same 16 of W3), so that gate and up of a
+// column meet in one warp; that needs N to be a multiple of 16, other N take the full tile.
+// Tiles are numbered group-major, then n-tile, then m-tile fastest, so that the pairs running together
+// share weight tiles through L2; groups of a single m-tile (streams of weights) are interleaved with
+// the others in proportion.  Pair i takes tiles i, i + pairs, ...
+// Every wait is bounded (kWaitTimeoutNs); one that gives up sets the error word and ends all roles.
 #include <algorithm>
+#include <cstring>
 
 #include "common.cuh"
 
 namespace colibri {
 namespace {
 
-constexpr int kTile = 64;       // rows and output columns of a tile
-constexpr int kChunk = 64;      // bytes of k per step
-constexpr int kPitch = kChunk + 4;
+// Set by a bounded wait that gave up, when the caller brings no word of its own.
+__device__ uint32_t g_int_err;
 
-template <bool kSwiglu, typename Out>
-__global__ void __launch_bounds__(256) int_gemm_kernel(const IntGemmArgs a, Out* __restrict__ y) {
-  __shared__ int s_row0, s_end, s_e;
-  __shared__ __align__(16) int8_t sa[kTile * kPitch], sb[2][kTile * kPitch];
-  if (threadIdx.x == 0) {
-    int e = 0, tile = blockIdx.x, beg = 0, end = a.rows;
-    if (a.offsets) {
-      int prev = 0;
-      e = -1;
-      for (int g = 0; g < a.E; ++g) {
-        const int b = min(max(a.offsets[g], prev), a.rows), n = min(max(a.offsets[g + 1], b), a.rows);
-        prev = n;
-        const int mt = (n - b + kTile - 1) / kTile;
-        if (tile < mt) {
-          e = g;
-          beg = b;
-          end = n;
-          break;
-        }
-        tile -= mt;
+constexpr int kThreads = 192;
+constexpr int kEpiThreads = 128;
+constexpr int kBM = 256;             // rows of a pair tile
+constexpr int kBN = 256;             // weight rows of a pair tile
+constexpr int kKB = 128;             // bytes of k per stage: one 128-byte swizzle atom
+constexpr int kHalf = 128 * kKB;     // 16 KB: this CTA's A or B part of a stage
+constexpr int kStage = 2 * kHalf;
+constexpr int kStages = 6;
+constexpr int kLightRows = 128;      // swapped tiles: at most 64 token rows per CTA
+constexpr int kDenseRows = 32;       // swapped tiles with two k blocks per stage
+constexpr int kTok = 16 * kKB;       // a 16-row box of token rows
+constexpr int kTmemCols = 512;
+
+struct alignas(64) PairParams {
+  CUtensorMap mapA, mapA16, mapA32, mapA64;  // rows, in boxes of 128, 16, 32 and 64
+  CUtensorMap mapB;                          // weights, 128-row boxes
+  CUtensorMap mapB16;                        // SwiGLU: boxes of 4 x (16 W1 rows, the same 16 W3 rows)
+  const int32_t* offsets;
+  const float* a_scale;
+  const float* w_scale;
+  int64_t s_stride;
+  void* y;
+  int64_t ldy;
+  uint32_t* err;
+  int E, rows, N;
+  int n_tiles, num_kb;
+  int light_rows;  // m-tiles with at most this many rows run swapped (0: none)
+  bool vec;        // rows of y are 16-byte aligned
+};
+
+struct PairSmem {
+  uint64_t full[kStages];   // used in the leader: both CTAs' copies
+  uint64_t empty[kStages];  // per CTA: freed by the leader's multicast commit
+  uint64_t tfull[2];        // per CTA: accumulator ready (multicast commit)
+  uint64_t tempty[2];       // used in the leader: 8 epilogue warps
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int32_t off[kMaxExperts + 1];
+  int32_t mt[kMaxExperts + 1];  // m-tile prefix over all groups,
+  int32_t hv[kMaxExperts + 1];  // over groups with two or more m-tiles,
+  int32_t lt[kMaxExperts + 1];  // over groups with exactly one
+  float col[2][kBN];            // column scales of the tile (SwiGLU: gate | up)
+  float row[2][kLightRows];     // row scales of a swapped tile
+};
+constexpr size_t kPairTok = (size_t)kStages * 2 * kTok;
+constexpr size_t kPairSmem = (size_t)kStages * kStage + kPairTok + sizeof(PairSmem);
+static_assert(kPairSmem <= 232448, "shared memory of one CTA");
+
+struct Tile {
+  int e, row0, row_end, n0, mtiles;
+};
+
+// Group offsets (entry i counts as the largest of entries 0..i, within [0, rows]) and the m-tile
+// prefixes; one full warp.
+__device__ void pair_schedule(PairSmem& m, const PairParams& p) {
+  const int lane = threadIdx.x & 31;
+  int top = 0, all = 0, heavy = 0, light = 0;
+  if (lane == 0) m.mt[0] = m.hv[0] = m.lt[0] = 0;
+  if (!p.offsets) {
+    if (lane == 0) {
+      const int mt = (p.rows + kBM - 1) / kBM;
+      m.off[0] = 0;
+      m.off[1] = p.rows;
+      m.mt[1] = mt;
+      m.hv[1] = mt >= 2 ? mt : 0;
+      m.lt[1] = mt == 1 ? 1 : 0;
+    }
+    return;
+  }
+  for (int e0 = 0; e0 <= p.E; e0 += 32) {
+    const int i = e0 + lane;
+    int v = i <= p.E ? min(max(p.offsets[i], 0), p.rows) : 0;
+    v = max(v, top);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, a);
+    }
+    const int prev = __shfl_up_sync(0xffffffffu, v, 1);
+    const int before = lane == 0 ? top : prev;
+    // group i - 1 ends at entry i
+    const int mt = i >= 1 && i <= p.E ? (v - before + kBM - 1) / kBM : 0;
+    int a = mt, h = mt >= 2 ? mt : 0, l = mt == 1 ? 1 : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, h, o),
+                z = __shfl_up_sync(0xffffffffu, l, o);
+      if (lane >= o) {
+        a += x;
+        h += y;
+        l += z;
       }
     }
-    s_e = e;
-    s_row0 = beg + tile * kTile;
-    s_end = end;
+    if (i <= p.E) {
+      m.off[i] = v;
+      m.mt[i] = all + a;
+      m.hv[i] = heavy + h;
+      m.lt[i] = light + l;
+    }
+    top = __shfl_sync(0xffffffffu, v, 31);
+    all += __shfl_sync(0xffffffffu, a, 31);
+    heavy += __shfl_sync(0xffffffffu, h, 31);
+    light += __shfl_sync(0xffffffffu, l, 31);
   }
+}
+
+// largest e in [0, E) with pre[e] * n_tiles <= L
+__device__ __forceinline__ int find_group(const int32_t* pre, int E, int n_tiles, int L) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] * n_tiles <= L) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ Tile pair_tile(const PairParams& p, const PairSmem& m, int L, int ncols) {
+  const int nh = m.hv[p.E] * p.n_tiles, nl = m.lt[p.E] * p.n_tiles;
+  const int32_t* pre = m.mt;
+  int idx = L;
+  if (nh > 0 && nl > 0) {
+    const long long tot = (long long)nh + nl;
+    const int b = (int)((long long)L * nl / tot);
+    const bool light = (int)((long long)(L + 1) * nl / tot) > b;
+    pre = light ? m.lt : m.hv;
+    idx = light ? b : L - b;
+  }
+  Tile t;
+  t.e = find_group(pre, p.E, p.n_tiles, idx);
+  t.mtiles = m.mt[t.e + 1] - m.mt[t.e];
+  const int r = idx - pre[t.e] * p.n_tiles, n = r / t.mtiles, mm = r - n * t.mtiles;
+  t.row0 = m.off[t.e] + mm * kBM;
+  t.row_end = m.off[t.e + 1];
+  t.n0 = n * ncols;
+  return t;
+}
+
+// Bounded wait that also gives up as soon as another role has aborted (kCluster: acquire at cluster
+// scope, for barriers the other CTA of the pair arrives on).
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  auto try_wait = [&]() { return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (try_wait()) return true;
+  const unsigned long long t0 = global_ns();
+  uint32_t n = 0;
+  while (true) {
+    if (try_wait()) return true;
+    if ((++n & 255u) == 0) {
+      if (*abort_flag) return false;
+      if (global_ns() - t0 > kWaitTimeoutNs) return false;
+    }
+  }
+}
+
+template <typename Smem>
+__device__ __forceinline__ void raise_abort(Smem& m, uint32_t* err) {
+  *(volatile int*)&m.abort = 1;
+  atomicOr(err, kErrWaitTimeout);
+}
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 32 bits, 16 consecutive columns per thread, as integers
+__device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int (&v)[16]) {
+  float f[16];
+  tmem_ld16(taddr, f);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __float_as_int(f[i]);
+}
+
+// 16 consecutive values of a row; `n`: how many of them exist
+template <typename Out>
+__device__ __forceinline__ void store16(Out* dst, const float (&v)[16], int n, bool vec) {
+  if (vec && n >= 16) {
+    if constexpr (sizeof(Out) == 2) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) dst[i] = from_f32<Out>(v[i]);
+  }
+}
+
+template <bool kSwiglu, typename Out>
+__global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_constant__ PairParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint32_t* err = p.err ? p.err : &g_int_err;
+  // The 128-byte swizzle needs 1024-byte aligned stages; the dynamic shared window of a CTA starts
+  // 1024-byte aligned (both CTAs of a pair take this branch together).
+  if (smem_u32(smem) & 1023u) {
+    pdl_wait();
+    if (threadIdx.x == 0) atomicOr(err, kErrWaitTimeout);
+    return;
+  }
+  uint8_t* tok_base = smem + (size_t)kStages * kStage;  // [kStages][2] token boxes of dense swapped tiles
+  PairSmem& m = *reinterpret_cast<PairSmem*>(smem + (size_t)kStages * kStage + kPairTok);
+  volatile int* abort_flag = &m.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = (int)cluster_id_x(), npairs = (int)num_clusters_x();
+  constexpr int kCols = kSwiglu ? kBN / 2 : kBN;  // output columns of a tile
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&m.full[s], 1);
+      mbar_init(&m.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&m.tfull[a], 1);
+      mbar_init(&m.tempty[a], 8);
+    }
+    mbar_init(&m.drain, 1);
+    m.abort = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&p.mapA);
+    tma_prefetch_desc(&p.mapB);
+  }
+  pdl_wait();  // below: reads of earlier kernels' output; TMEM once the previous kernel released its own
+  if (warp == 1) {
+    tmem_alloc_pair(&m.tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+    tc_fence_before();
+  }
+  if (warp == 0) pair_schedule(m, p);
   __syncthreads();
-  if (s_e < 0 || s_row0 >= s_end) return;
-  const int row0 = s_row0, row_end = s_end, e = s_e, n0 = blockIdx.y * kTile;
-  const int8_t* W = a.W + (size_t)e * a.w_stride;
-  const float* ws = a.w_scale + (size_t)e * a.s_stride;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[2][4][4] = {};
-  const int lr = threadIdx.x >> 2, lc = (threadIdx.x & 3) * 16;
-  for (int k0 = 0; k0 < a.K; k0 += kChunk) {
-    const bool kin = k0 + lc < a.K;
-    uint4 va = make_uint4(0, 0, 0, 0), vb[2] = {va, va};
-    if (kin && row0 + lr < row_end) va = *reinterpret_cast<const uint4*>(a.A + (size_t)(row0 + lr) * a.lda + k0 + lc);
-    if (kin && n0 + lr < a.N) {
-      vb[0] = *reinterpret_cast<const uint4*>(W + (size_t)(n0 + lr) * a.ldw + k0 + lc);
-      if (kSwiglu) vb[1] = *reinterpret_cast<const uint4*>(W + (size_t)(a.N + n0 + lr) * a.ldw + k0 + lc);
-    }
-    __syncthreads();
-    auto put = [&](int8_t* dst, const uint4& v) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(dst + lr * kPitch + lc);
-      p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
-    };
-    put(sa, va);
-    put(sb[0], vb[0]);
-    if (kSwiglu) put(sb[1], vb[1]);
-    __syncthreads();
-#pragma unroll 4
-    for (int k = 0; k < kChunk; k += 4) {
-      int av[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) av[i] = *reinterpret_cast<const int*>(sa + (ty + 16 * i) * kPitch + k);
-#pragma unroll
-      for (int m = 0; m < (kSwiglu ? 2 : 1); ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int bv = *reinterpret_cast<const int*>(sb[m] + (tx + 16 * j) * kPitch + k);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][i][j] = __dp4a(av[i], bv, acc[m][i][j]);
+  cluster_sync_all();  // the peer's barriers are initialised before any cross-CTA arrival
+  tc_fence_after();
+  const uint32_t tmem_base = m.tmem_base;
+  const int total = m.mt[p.E] * p.n_tiles;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- TMA producer (both CTAs)
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      const uint64_t evict_first = l2_evict_first_policy();
+      bool ok = true;
+      for (int L = pair; ok && L < total; L += npairs) {
+        const Tile t = pair_tile(p, m, L, kCols);
+        const int trows = t.row_end - t.row0;
+        const bool light = trows <= p.light_rows, dense = light && trows <= kDenseRows;
+        const bool once = light && t.mtiles == 1;  // its weights are read by this tile alone: evict them first
+        const int nh = (trows + 31) / 32 * 16;     // swapped: token rows (N / 2) per CTA
+        const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
+        for (int step = 0; step < steps; ++step) {
+          if (!wait_or_abort(&m.empty[s], ph ^ 1u, abort_flag)) {
+            raise_abort(m, err);
+            ok = false;
+            break;
+          }
+          uint8_t* sA = smem + (size_t)s * kStage;
+          uint8_t* sB = sA + kHalf;
+          const uint32_t bar = mapa_shared(smem_u32(&m.full[s]), 0);
+          // 128 weight rows of a swapped tile
+          auto weights = [&](uint8_t* dst, int kx) {
+            if (kSwiglu) {
+              if (once) tma2_load_5d_hint(dst, &p.mapB16, bar, kx, 0, 0, (t.n0 + 64 * (int)rank) / 16, t.e, evict_first);
+              else tma2_load_5d(dst, &p.mapB16, bar, kx, 0, 0, (t.n0 + 64 * (int)rank) / 16, t.e);
+            } else {
+              if (once) tma2_load_3d_hint(dst, &p.mapB, bar, kx, t.n0 + 128 * (int)rank, t.e, evict_first);
+              else tma2_load_3d(dst, &p.mapB, bar, kx, t.n0 + 128 * (int)rank, t.e);
+            }
+          };
+          if (dense) {
+            const int nk = min(2, p.num_kb - 2 * step);
+            if (rank == 0) mbar_arrive_expect_tx(&m.full[s], (uint32_t)(2 * nk * (kHalf + kTok)));
+            for (int j = 0; j < nk; ++j) {
+              const int kx = (2 * step + j) * kKB;
+              weights(sA + (size_t)j * kHalf, kx);
+              tma2_load_2d(tok_base + (size_t)(2 * s + j) * kTok, &p.mapA16, bar, kx, t.row0 + (int)rank * nh);
+            }
+          } else if (light) {
+            const int box = nh <= 32 ? 32 : 64;
+            if (rank == 0) mbar_arrive_expect_tx(&m.full[s], (uint32_t)(2 * (kHalf + box * kKB)));
+            weights(sA, step * kKB);
+            tma2_load_2d(sB, nh <= 32 ? &p.mapA32 : &p.mapA64, bar, step * kKB, t.row0 + (int)rank * nh);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(&m.full[s], 2 * kStage);
+            tma2_load_2d(sA, &p.mapA, bar, step * kKB, t.row0 + 128 * (int)rank);
+            if (kSwiglu) tma2_load_4d(sB, &p.mapB, bar, step * kKB, t.n0, (int)rank, t.e);
+            else tma2_load_3d(sB, &p.mapB, bar, step * kKB, t.n0 + 128 * (int)rank, t.e);
+          }
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
+      }
+    }
+    pdl_trigger();  // every copy of this CTA is issued: let the next kernel be scheduled
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA issuer (leader only)
+    if (lane == 0 && rank == 0) {
+      int s = 0, it = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int L = pair; ok && L < total; L += npairs, ++it) {
+        const Tile t = pair_tile(p, m, L, kCols);
+        const int a = it & 1;
+        if (!wait_or_abort<true>(&m.tempty[a], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(a * kBN);
+        const int trows = t.row_end - t.row0;
+        const bool light = trows <= p.light_rows, dense = light && trows <= kDenseRows;
+        const uint32_t idesc = light ? idesc_s8_s32(kBM, (trows + 31) / 32 * 32) : idesc_s8_s32(kBM, kBN);
+        const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
+        for (int step = 0; step < steps; ++step) {
+          if (!wait_or_abort<true>(&m.full[s], ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sA = smem_u32(smem + (size_t)s * kStage);
+          if (dense) {
+            const int nk = min(2, p.num_kb - 2 * step);
+            for (int j = 0; j < nk; ++j) {
+              const uint32_t wa = sA + (uint32_t)(j * kHalf), tb = smem_u32(tok_base + (size_t)(2 * s + j) * kTok);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_i8_pair(d_tmem, smem_desc_sw128(wa + kk * 32), smem_desc_sw128(tb + kk * 32), idesc,
+                               (step | j | kk) != 0 ? 1u : 0u);
+            }
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_i8_pair(d_tmem, smem_desc_sw128(sA + kk * 32), smem_desc_sw128(sA + kHalf + kk * 32), idesc,
+                             (step | kk) != 0 ? 1u : 0u);
+          }
+          tc_commit_pair_mc(&m.empty[s], 0x3);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) tc_commit_pair_mc(&m.tfull[a], 0x3);
+      }
+      if (!ok) raise_abort(m, err);
+      tc_commit_pair(&m.drain);
+      mbar_wait_bounded(&m.drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- epilogue (warps 2..5, both CTAs)
+    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    const int tid = threadIdx.x - 64;
+    Out* const y = static_cast<Out*>(p.y);
+    int it = 0;
+    bool dead = false;  // after a wait that gave up: only the barriers below are kept up
+    for (int L = pair; L < total; L += npairs, ++it) {
+      const Tile t = pair_tile(p, m, L, kCols);
+      const int a = it & 1, trows = t.row_end - t.row0;
+      const bool light = trows <= p.light_rows;
+      // the tile's scales (the other copy may still be read by a slower warp)
+      const float* ws = p.w_scale + (size_t)t.e * p.s_stride;
+      for (int c = tid; c < kBN; c += kEpiThreads) {
+        const int n = t.n0 + (kSwiglu ? c & (kBN / 2 - 1) : c);
+        m.col[a][c] = n < p.N ? __ldg(ws + (kSwiglu && c >= kBN / 2 ? p.N : 0) + n) : 0.f;
+      }
+      if (light) m.row[a][tid] = tid < trows ? __ldg(p.a_scale + t.row0 + tid) : 0.f;
+      const int row = t.row0 + 128 * (int)rank + q * 32 + lane;
+      const bool valid = row < t.row_end;
+      const float sr = !light && valid ? __ldg(p.a_scale + row) : 0.f;
+      epilogue_sync();
+      if (!dead) {
+        const bool got = wait_or_abort(&m.tfull[a], (uint32_t)(it >> 1) & 1u, abort_flag);
+        dead = !__all_sync(0xffffffffu, got);
+        if (dead && lane == 0) raise_abort(m, err);
+      }
+      if (dead) continue;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * kBN);
+      const float* col = m.col[a];
+      if (light) {
+        // TMEM lane = weight row of this CTA, column c = the tile's row t.row0 + c
+        const float* rs = m.row[a];
+        if (kSwiglu) {
+          // lanes 0-15: gate of column 64 rank + 16 q + lane, lanes 16-31: up of the same columns
+          const int c0 = 64 * (int)rank + 16 * q + (lane & 15), oc = t.n0 + c0;
+          const float tn = col[(lane < 16 ? 0 : kBN / 2) + c0];
+          for (int c = 0; c < trows; c += 16) {
+            int v[16];
+            tmem_ld16i(tb + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = c + i < trows ? (float)v[i] * (rs[(c + i) & (kLightRows - 1)] * tn) : 0.f;
+              const float up = __shfl_down_sync(0xffffffffu, x, 16);
+              if (lane < 16 && c + i < trows && oc < p.N)
+                y[(int64_t)(t.row0 + c + i) * p.ldy + oc] = from_f32<Out>(silu_mul(x, up));
+            }
+          }
+        } else {
+          const int c0 = 128 * (int)rank + q * 32 + lane, oc = t.n0 + c0;
+          const float tn = col[c0];
+          for (int c = 0; c < trows; c += 16) {
+            int v[16];
+            tmem_ld16i(tb + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c + i < trows && oc < p.N)
+                y[(int64_t)(t.row0 + c + i) * p.ldy + oc] = from_f32<Out>((float)v[i] * (rs[c + i] * tn));
+          }
+        }
+      } else {
+        Out* const out = y + (int64_t)row * p.ldy + t.n0;
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 16) {
+          int g[16], u[16];
+          tmem_ld16i(tb + c, g);
+          if (kSwiglu) tmem_ld16i(tb + kBN / 2 + c, u);
+          tmem_ld_wait();
+          const int left = p.N - t.n0 - c;
+          if (valid && left > 0) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              v[i] = (float)g[i] * (sr * col[c + i]);
+              if (kSwiglu) v[i] = silu_mul(v[i], (float)u[i] * (sr * col[kBN / 2 + c + i]));
+            }
+            store16(out + c, v, left, p.vec);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&m.tempty[a]), 0));
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = row0 + ty + 16 * i;
-    if (r >= row_end) continue;
-    const float sr = a.a_scale[r];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx + 16 * j;
-      if (n >= a.N) continue;
-      float v = (float)acc[0][i][j] * (sr * ws[n]);
-      if (kSwiglu) v = silu_mul(v, (float)acc[1][i][j] * (sr * ws[a.N + n]));
-      y[(size_t)r * a.ldy + n] = from_f32<Out>(v);
+
+  __syncthreads();
+  if (threadIdx.x == 0 && m.abort) {
+    // error path: give copies still in flight time to land before the CTA leaves
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 2000000ull) {
     }
   }
+  cluster_sync_all();  // the peer no longer reads this CTA's shared memory or arrives on it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+bool byte_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+              const uint32_t* box) {
+  return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides, box);
+}
+
+template <bool kSwiglu>
+cudaError_t launch_pair(const IntGemmArgs& a, cudaStream_t s) {
+  PairParams p;
+  memset(&p, 0, sizeof(p));
+  const uint64_t K = a.K, N = a.N, E = a.E;
+  const uint64_t es = a.w_stride > 0 ? (uint64_t)a.w_stride : (uint64_t)a.ldw;  // a single group: not used
+  bool ok = true;
+  {
+    uint64_t dims[2] = {K, (uint64_t)a.rows}, st[1] = {(uint64_t)a.lda};
+    uint32_t box[2] = {kKB, 128};
+    ok &= byte_map(&p.mapA, a.A, 2, dims, st, box);
+    box[1] = 16;
+    ok &= byte_map(&p.mapA16, a.A, 2, dims, st, box);
+    box[1] = 32;
+    ok &= byte_map(&p.mapA32, a.A, 2, dims, st, box);
+    box[1] = 64;
+    ok &= byte_map(&p.mapA64, a.A, 2, dims, st, box);
+  }
+  p.light_rows = kLightRows;
+  if (kSwiglu) {
+    uint64_t dims[4] = {K, N, 2, E}, st[3] = {K, N * K, es};
+    uint32_t box[4] = {kKB, 128, 1, 1};
+    ok &= byte_map(&p.mapB, a.W, 4, dims, st, box);
+    if (N % 16 == 0) {
+      uint64_t dims16[5] = {K, 16, 2, N / 16, E}, st16[4] = {K, N * K, 16 * K, es};
+      uint32_t box16[5] = {kKB, 16, 2, 4, 1};
+      ok &= byte_map(&p.mapB16, a.W, 5, dims16, st16, box16);
+    } else {
+      p.light_rows = 0;
+    }
+  } else {
+    uint64_t dims[3] = {K, N, E}, st[2] = {(uint64_t)a.ldw, es};
+    uint32_t box[3] = {kKB, 128, 1};
+    ok &= byte_map(&p.mapB, a.W, 3, dims, st, box);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  p.offsets = a.offsets;
+  p.a_scale = a.a_scale;
+  p.w_scale = a.w_scale;
+  p.s_stride = a.s_stride;
+  p.y = a.y;
+  p.ldy = a.ldy;
+  p.err = a.err;
+  p.E = a.E;
+  p.rows = a.rows;
+  p.N = a.N;
+  p.num_kb = (a.K + kKB - 1) / kKB;
+  const int cols = kSwiglu ? kBN / 2 : kBN, osize = a.out_dtype == COLIBRI_BF16 ? 2 : 4;
+  p.n_tiles = (a.N + cols - 1) / cols;
+  p.vec = (a.ldy * osize) % 16 == 0;
+  const long long bound = (long long)(a.rows / kBM + (a.offsets ? a.E : 1)) * p.n_tiles;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const unsigned pairs = (unsigned)std::min<long long>(bound, sms / 2);
+  auto kern = a.out_dtype == COLIBRI_BF16 ? i8_pair_kernel<kSwiglu, __nv_bfloat16> : i8_pair_kernel<kSwiglu, float>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(2 * pairs), dim3(kThreads), kPairSmem, s, 2, p);
 }
 
 }  // namespace
 
 cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s) {
   if (a.rows <= 0) return cudaSuccess;
-  const dim3 grid(a.rows / kTile + (a.offsets ? a.E : 1), (a.N + kTile - 1) / kTile), block(256);
-  if (a.out_dtype == COLIBRI_BF16) {
-    __nv_bfloat16* y = (__nv_bfloat16*)a.y;
-    return swiglu ? launch_kernel(int_gemm_kernel<true, __nv_bfloat16>, grid, block, 0, s, 1, a, y)
-                  : launch_kernel(int_gemm_kernel<false, __nv_bfloat16>, grid, block, 0, s, 1, a, y);
-  }
-  float* y = (float*)a.y;
-  return swiglu ? launch_kernel(int_gemm_kernel<true, float>, grid, block, 0, s, 1, a, y)
-                : launch_kernel(int_gemm_kernel<false, float>, grid, block, 0, s, 1, a, y);
+  return swiglu ? launch_pair<true>(a, s) : launch_pair<false>(a, s);
+}
+
+// The error word of calls without one of their own, read and cleared (after `s` is idle).
+cudaError_t int_gemm_take_error(uint32_t* word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_int_err, sizeof(uint32_t));
+  const uint32_t zero = 0;
+  if (e == cudaSuccess && *word) e = cudaMemcpyToSymbol(g_int_err, &zero, sizeof(zero));
+  return e;
 }
 
 }  // namespace colibri

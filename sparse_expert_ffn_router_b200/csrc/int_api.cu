@@ -101,7 +101,7 @@ colibri_status experts(bool swiglu, const int8_t* A, int64_t lda, const float* a
   if (rows == 0) return COLIBRI_OK;
   COLIBRI_CHECK(check_buffers({Buf{"A", A}, Buf{"a_scale", a_scale}, Buf{"offsets", offsets}, Buf{"W", W},
                                Buf{"w_scale", w_scale}, Buf{"y", y}}));
-  IntGemmArgs a{A, lda, a_scale, rows, offsets, E, W, w_stride, K, w_scale, s_stride, N, K, y, ldy, out_dtype};
+  IntGemmArgs a{A, lda, a_scale, rows, offsets, E, W, w_stride, K, w_scale, s_stride, N, K, y, ldy, out_dtype, nullptr};
   return launched(launch_int_gemm(a, swiglu, reinterpret_cast<cudaStream_t>(stream)), "int8 expert product");
 }
 
@@ -131,7 +131,7 @@ colibri_status colibri_int_gemm(const int8_t* A, int64_t lda, const float* a_sca
   COLIBRI_CHECK(check_ld("ldy", ldy, N, out_dtype == COLIBRI_F32 ? 4 : 2, false));
   if (M == 0) return COLIBRI_OK;
   COLIBRI_CHECK(check_buffers({Buf{"A", A}, Buf{"a_scale", a_scale}, Buf{"W", W}, Buf{"w_scale", w_scale}, Buf{"y", y}}));
-  IntGemmArgs a{A, lda, a_scale, M, nullptr, 1, W, 0, ldw, w_scale, 0, N, K, y, ldy, out_dtype};
+  IntGemmArgs a{A, lda, a_scale, M, nullptr, 1, W, 0, ldw, w_scale, 0, N, K, y, ldy, out_dtype, nullptr};
   return launched(launch_int_gemm(a, false, reinterpret_cast<cudaStream_t>(stream)), "int8 product");
 }
 
@@ -149,6 +149,18 @@ colibri_status colibri_int_swiglu_experts(const int8_t* A, int64_t lda, const fl
                                           int32_t K, void* h, int64_t ldh, int32_t out_dtype, void* stream) {
   return experts(true, A, lda, a_scale, rows, offsets, num_experts, W, w_stride, w_scale, s_stride, N, K, h, ldh,
                  out_dtype, stream);
+}
+
+colibri_status colibri_int_check(void* stream) {
+  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return refuse(COLIBRI_ERR_CUDA, "stream synchronize failed");
+  }
+  uint32_t word = 0;
+  const cudaError_t e = int_gemm_take_error(&word);
+  if (e != cudaSuccess) return launched(e, "reading the error word");
+  if (word) return refuse(COLIBRI_ERR_TIMEOUT, "a bounded device wait of an int8 product gave up");
+  return COLIBRI_OK;
 }
 
 }  // extern "C"
