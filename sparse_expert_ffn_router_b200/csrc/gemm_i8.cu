@@ -8,13 +8,15 @@
 // fp32 and the two scales round once each, and the result once to its type.
 //
 // i8_pair_kernel: clusters of two CTAs (tcgen05 cta_group::2, kind::i8), persistent, one pair per two
-// SMs, 192 threads per CTA:
+// SMs, 224 threads per CTA:
 //   warp 0      TMA producer: this CTA's 128 rows of A and 128 of the 256 weight rows of the tile
 //               (SwiGLU: the leader W1, the peer W3), 128 bytes of k per stage, into a ring of 32 KB
 //               stages; both CTAs' copies count on the leader's barrier.
 //   warp 1      the leader issues the M = 256, N = 256, K = 32 MMAs, four per stage, into one of two
 //               accumulators (128 rows x 256 int32 columns of TMEM in each CTA).
 //   warps 2-5   epilogue: TMEM -> registers, scales, SwiGLU, stores; it overlaps the next tile's MMAs.
+//   warp 6      planner: finds the tiles ahead of the other roles and fetches their scales (done by the
+//               roles themselves this cost 1.5 us between two tiles of MMAs and 3 us per epilogue)
 // A group's last m-tile of at most 128 rows runs with the operands swapped (weights the M side, its
 // rows rounded up to 32 the N side), so that a group of a few rows costs the stream of its weights
 // and little else; with at most 32 rows a stage holds two k blocks of weights.  For SwiGLU a swapped
@@ -35,8 +37,11 @@ namespace {
 // Set by a bounded wait that gave up, when the caller brings no word of its own.
 __device__ uint32_t g_int_err;
 
-constexpr int kThreads = 192;
-constexpr int kEpiThreads = 128;
+// (two warps per quarter of the TMEM lanes measured slower: expert gate/up 788 against 730 us)
+constexpr int kEpiWarps = 4;
+constexpr int kEpiThreads = 32 * kEpiWarps;
+constexpr int kThreads = 96 + kEpiThreads;
+constexpr int kPlans = 4;            // tiles the planner may be ahead
 constexpr int kBM = 256;             // rows of a pair tile
 constexpr int kBN = 256;             // weight rows of a pair tile
 constexpr int kKB = 128;             // bytes of k per stage: one 128-byte swizzle atom
@@ -47,6 +52,7 @@ constexpr int kLightRows = 128;      // swapped tiles: at most 64 token rows per
 constexpr int kDenseRows = 32;       // swapped tiles with two k blocks per stage
 constexpr int kTok = 16 * kKB;       // a 16-row box of token rows
 constexpr int kTmemCols = 512;
+constexpr int kStagePitch = 17;
 
 struct alignas(64) PairParams {
   CUtensorMap mapA, mapA16, mapA32, mapA64;  // rows, in boxes of 128, 16, 32 and 64
@@ -62,14 +68,22 @@ struct alignas(64) PairParams {
   int E, rows, N;
   int n_tiles, num_kb;
   int light_rows;  // m-tiles with at most this many rows run swapped (0: none)
+  int dense_rows;  // ... and with at most this many, two k blocks per stage
   bool vec;        // rows of y are 16-byte aligned
+};
+
+struct Tile {
+  int e, row0, row_end, n0, mtiles;
 };
 
 struct PairSmem {
   uint64_t full[kStages];   // used in the leader: both CTAs' copies
   uint64_t empty[kStages];  // per CTA: freed by the leader's multicast commit
   uint64_t tfull[2];        // per CTA: accumulator ready (multicast commit)
-  uint64_t tempty[2];       // used in the leader: 8 epilogue warps
+  uint64_t tempty[2];       // used in the leader: both CTAs' epilogue warps
+  uint64_t ifull[kPlans];   // tile found
+  uint64_t sfull[kPlans];   // its scales are there
+  uint64_t pfree[kPlans];   // producer, MMA thread (leader) and epilogue warps are done with it
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -77,68 +91,79 @@ struct PairSmem {
   int32_t mt[kMaxExperts + 1];  // m-tile prefix over all groups,
   int32_t hv[kMaxExperts + 1];  // over groups with two or more m-tiles,
   int32_t lt[kMaxExperts + 1];  // over groups with exactly one
-  float col[2][kBN];            // column scales of the tile (SwiGLU: gate | up)
-  float row[2][kLightRows];     // row scales of a swapped tile
+  Tile tile[kPlans];
+  alignas(16) float col[kPlans][kBN];  // column scales of the tile (SwiGLU: gate | up)
+  alignas(16) float row[kPlans][128];  // row scales: of this CTA's rows, or of a swapped tile's
 };
 constexpr size_t kPairTok = (size_t)kStages * 2 * kTok;
 constexpr size_t kPairSmem = (size_t)kStages * kStage + kPairTok + sizeof(PairSmem);
 static_assert(kPairSmem <= 232448, "shared memory of one CTA");
-
-struct Tile {
-  int e, row0, row_end, n0, mtiles;
-};
+static_assert(kEpiWarps * 32 * kStagePitch * 4 <= kPairTok, "transposes");
 
 // Group offsets (entry i counts as the largest of entries 0..i, within [0, rows]) and the m-tile
 // prefixes; one full warp.
 __device__ void pair_schedule(PairSmem& m, const PairParams& p) {
   const int lane = threadIdx.x & 31;
-  int top = 0, all = 0, heavy = 0, light = 0;
-  if (lane == 0) m.mt[0] = m.hv[0] = m.lt[0] = 0;
-  if (!p.offsets) {
-    if (lane == 0) {
-      const int mt = (p.rows + kBM - 1) / kBM;
-      m.off[0] = 0;
-      m.off[1] = p.rows;
-      m.mt[1] = mt;
-      m.hv[1] = mt >= 2 ? mt : 0;
-      m.lt[1] = mt == 1 ? 1 : 0;
-    }
-    return;
+  constexpr int kPer = kMaxExperts / 32;
+  const int per = (p.E + 31) / 32, e0 = lane * per;  // this lane's groups
+  int end[kPer];                                     // entry e0 + i + 1
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    end[i] = 0;
+    if (i < per && e0 + i < p.E) end[i] = p.offsets ? min(max(p.offsets[e0 + i + 1], 0), p.rows) : p.rows;
   }
-  for (int e0 = 0; e0 <= p.E; e0 += 32) {
-    const int i = e0 + lane;
-    int v = i <= p.E ? min(max(p.offsets[i], 0), p.rows) : 0;
-    v = max(v, top);
+  int first = 0;
+  if (lane == 0 && p.offsets) first = min(max(p.offsets[0], 0), p.rows);
+  int top = first;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v = max(v, a);
-    }
-    const int prev = __shfl_up_sync(0xffffffffu, v, 1);
-    const int before = lane == 0 ? top : prev;
-    // group i - 1 ends at entry i
-    const int mt = i >= 1 && i <= p.E ? (v - before + kBM - 1) / kBM : 0;
-    int a = mt, h = mt >= 2 ? mt : 0, l = mt == 1 ? 1 : 0;
+  for (int i = 0; i < kPer; ++i) top = max(top, end[i]);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, h, o),
-                z = __shfl_up_sync(0xffffffffu, l, o);
-      if (lane >= o) {
-        a += x;
-        h += y;
-        l += z;
-      }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, top, o);
+    if (lane >= o) top = max(top, v);
+  }
+  int begin = __shfl_up_sync(0xffffffffu, top, 1);  // where this lane's first group begins
+  if (lane == 0) begin = first;
+  int all = 0, heavy = 0;
+  int at = begin;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (i < per && e0 + i < p.E) {
+      const int to = max(at, end[i]), mt = (to - at + kBM - 1) / kBM;
+      end[i] = to;
+      all += mt;
+      heavy += mt >= 2 ? mt : 0;
+      at = to;
     }
-    if (i <= p.E) {
-      m.off[i] = v;
-      m.mt[i] = all + a;
-      m.hv[i] = heavy + h;
-      m.lt[i] = light + l;
+  }
+  int ia = all, ih = heavy;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ih, o);
+    if (lane >= o) {
+      ia += x;
+      ih += y;
     }
-    top = __shfl_sync(0xffffffffu, v, 31);
-    all += __shfl_sync(0xffffffffu, a, 31);
-    heavy += __shfl_sync(0xffffffffu, h, 31);
-    light += __shfl_sync(0xffffffffu, l, 31);
+  }
+  all = ia - all;
+  heavy = ih - heavy;
+  if (lane == 0) {
+    m.off[0] = first;
+    m.mt[0] = m.hv[0] = m.lt[0] = 0;
+  }
+  at = begin;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (i < per && e0 + i < p.E) {
+      const int mt = (end[i] - at + kBM - 1) / kBM;
+      all += mt;
+      heavy += mt >= 2 ? mt : 0;
+      m.off[e0 + i + 1] = end[i];
+      m.mt[e0 + i + 1] = all;
+      m.hv[e0 + i + 1] = heavy;
+      m.lt[e0 + i + 1] = all - heavy;  // a group has one m-tile, or is heavy, or is empty
+      at = end[i];
+    }
   }
 }
 
@@ -197,8 +222,6 @@ __device__ __forceinline__ void raise_abort(Smem& m, uint32_t* err) {
   atomicOr(err, kErrWaitTimeout);
 }
 
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
 __device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
@@ -217,29 +240,55 @@ __device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __float_as_int(f[i]);
 }
 
-// 16 consecutive values of a row; `n`: how many of them exist
+// Waits for the loads of this warp from TMEM; the values pass through it, so that nothing computed from
+// them can be scheduled before it.
+__device__ __forceinline__ void tmem_ld_wait16(int (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+
+// silu(g) * u; the quotient by the approximate division (2 ulp)
+__device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// One warp: a block of 32 rows (lane = row) by 16 columns at `dst` (row 0, column 0), `rows` and `cols`
+// of which exist.  Rows that are 16-byte aligned and whole are written by their lanes; others are
+// transposed through shared memory so that the lanes write consecutive columns (a lane per row costs a
+// memory transaction per value: 32 us for the 256 x 256 tiles of an odd-width bf16 output, measured).
 template <typename Out>
-__device__ __forceinline__ void store16(Out* dst, const float (&v)[16], int n, bool vec) {
-  if (vec && n >= 16) {
-    if constexpr (sizeof(Out) == 2) {
-      uint32_t w[8];
+__device__ __forceinline__ void store_block(Out* dst, int64_t ldy, const float (&v)[16], int rows, int cols, bool vec,
+                                            float* stage, int lane) {
+  if (vec && cols >= 16) {
+    if (lane < rows) {
+      Out* d = dst + lane * ldy;
+      if constexpr (sizeof(Out) == 2) {
+        uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int i = 0; i < 8; ++i) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          reinterpret_cast<float4*>(d)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
       }
-      reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) dst[i] = from_f32<Out>(v[i]);
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) stage[lane * kStagePitch + i] = v[i];
+  __syncwarp();
+  const int n = min(rows, 32), c = lane & 15;
+  if (c < cols) {
+#pragma unroll 4
+    for (int r = lane >> 4; r < n; r += 2) dst[r * ldy + c] = from_f32<Out>(stage[r * kStagePitch + c]);
+  }
+  __syncwarp();
 }
 
 template <bool kSwiglu, typename Out>
@@ -268,7 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&m.tfull[a], 1);
-      mbar_init(&m.tempty[a], 8);
+      mbar_init(&m.tempty[a], 2 * kEpiWarps);
+    }
+    for (int i = 0; i < kPlans; ++i) {
+      mbar_init(&m.ifull[i], 1);
+      mbar_init(&m.sfull[i], 1);
+      mbar_init(&m.pfree[i], (rank == 0 ? 2 : 1) + kEpiWarps);
     }
     mbar_init(&m.drain, 1);
     m.abort = 0;
@@ -296,10 +350,17 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
       uint32_t ph = 0;
       const uint64_t evict_first = l2_evict_first_policy();
       bool ok = true;
-      for (int L = pair; ok && L < total; L += npairs) {
-        const Tile t = pair_tile(p, m, L, kCols);
+      int it = 0;
+      for (int L = pair; ok && L < total; L += npairs, ++it) {
+        const int slot = it % kPlans;
+        if (!wait_or_abort(&m.ifull[slot], (uint32_t)(it / kPlans) & 1u, abort_flag)) {
+          raise_abort(m, err);
+          break;
+        }
+        const Tile t = m.tile[slot];
+        mbar_arrive(&m.pfree[slot]);
         const int trows = t.row_end - t.row0;
-        const bool light = trows <= p.light_rows, dense = light && trows <= kDenseRows;
+        const bool light = trows <= p.light_rows, dense = trows <= p.dense_rows;
         const bool once = light && t.mtiles == 1;  // its weights are read by this tile alone: evict them first
         const int nh = (trows + 31) / 32 * 16;     // swapped: token rows (N / 2) per CTA
         const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
@@ -357,7 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
       uint32_t ph = 0;
       bool ok = true;
       for (int L = pair; ok && L < total; L += npairs, ++it) {
-        const Tile t = pair_tile(p, m, L, kCols);
+        const int slot = it % kPlans;
+        if (!wait_or_abort(&m.ifull[slot], (uint32_t)(it / kPlans) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const Tile t = m.tile[slot];
+        mbar_arrive(&m.pfree[slot]);
         const int a = it & 1;
         if (!wait_or_abort<true>(&m.tempty[a], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag)) {
           ok = false;
@@ -366,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(a * kBN);
         const int trows = t.row_end - t.row0;
-        const bool light = trows <= p.light_rows, dense = light && trows <= kDenseRows;
+        const bool light = trows <= p.light_rows, dense = trows <= p.dense_rows;
         const uint32_t idesc = light ? idesc_s8_s32(kBM, (trows + 31) / 32 * 32) : idesc_s8_s32(kBM, kBN);
         const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
         for (int step = 0; step < steps; ++step) {
@@ -404,40 +471,62 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
       mbar_wait_bounded(&m.drain, 0);
     }
     __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------------------------- planner (both CTAs)
+    int it = 0;
+    for (int L = pair; L < total; L += npairs, ++it) {
+      const int slot = it % kPlans;
+      const bool got = wait_or_abort(&m.pfree[slot], ((uint32_t)(it / kPlans) & 1u) ^ 1u, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) raise_abort(m, err);
+        break;
+      }
+      const Tile t = pair_tile(p, m, L, kCols);
+      if (lane == 0) {
+        m.tile[slot] = t;
+        mbar_arrive(&m.ifull[slot]);
+      }
+      const int trows = t.row_end - t.row0;
+      const float* ws = p.w_scale + (size_t)t.e * p.s_stride;
+      float cs[kBN / 32], rs[4];
+#pragma unroll
+      for (int i = 0; i < kBN / 32; ++i) {
+        const int c = lane + 32 * i, n = t.n0 + (kSwiglu ? c & (kBN / 2 - 1) : c);
+        cs[i] = n < p.N ? __ldg(ws + (kSwiglu && c >= kBN / 2 ? p.N : 0) + n) : 0.f;
+      }
+      const int r0 = trows <= p.light_rows ? t.row0 : t.row0 + 128 * (int)rank;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rs[i] = r0 + lane + 32 * i < t.row_end ? __ldg(p.a_scale + r0 + lane + 32 * i) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kBN / 32; ++i) m.col[slot][lane + 32 * i] = cs[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m.row[slot][lane + 32 * i] = rs[i];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.sfull[slot]);
+    }
   } else {
     // ------------------------------------------------------------- epilogue (warps 2..5, both CTAs)
     const int q = warp & 3;  // TMEM lane quarter this warp may access
-    const int tid = threadIdx.x - 64;
+    float* stage = reinterpret_cast<float*>(tok_base) + q * (32 * kStagePitch);  // used when dense_rows is 0
     Out* const y = static_cast<Out*>(p.y);
     int it = 0;
-    bool dead = false;  // after a wait that gave up: only the barriers below are kept up
     for (int L = pair; L < total; L += npairs, ++it) {
-      const Tile t = pair_tile(p, m, L, kCols);
-      const int a = it & 1, trows = t.row_end - t.row0;
-      const bool light = trows <= p.light_rows;
-      // the tile's scales (the other copy may still be read by a slower warp)
-      const float* ws = p.w_scale + (size_t)t.e * p.s_stride;
-      for (int c = tid; c < kBN; c += kEpiThreads) {
-        const int n = t.n0 + (kSwiglu ? c & (kBN / 2 - 1) : c);
-        m.col[a][c] = n < p.N ? __ldg(ws + (kSwiglu && c >= kBN / 2 ? p.N : 0) + n) : 0.f;
+      const int a = it & 1, slot = it % kPlans;
+      const bool got = wait_or_abort(&m.sfull[slot], (uint32_t)(it / kPlans) & 1u, abort_flag) &&
+                       wait_or_abort(&m.tfull[a], (uint32_t)(it >> 1) & 1u, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) raise_abort(m, err);
+        break;
       }
-      if (light) m.row[a][tid] = tid < trows ? __ldg(p.a_scale + t.row0 + tid) : 0.f;
-      const int row = t.row0 + 128 * (int)rank + q * 32 + lane;
-      const bool valid = row < t.row_end;
-      const float sr = !light && valid ? __ldg(p.a_scale + row) : 0.f;
-      epilogue_sync();
-      if (!dead) {
-        const bool got = wait_or_abort(&m.tfull[a], (uint32_t)(it >> 1) & 1u, abort_flag);
-        dead = !__all_sync(0xffffffffu, got);
-        if (dead && lane == 0) raise_abort(m, err);
-      }
-      if (dead) continue;
       tc_fence_after();
+      const Tile t = m.tile[slot];
+      const int trows = t.row_end - t.row0;
+      const bool light = trows <= p.light_rows;
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * kBN);
-      const float* col = m.col[a];
+      const float* col = m.col[slot];
       if (light) {
         // TMEM lane = weight row of this CTA, column c = the tile's row t.row0 + c
-        const float* rs = m.row[a];
+        const float* rs = m.row[slot];
         if (kSwiglu) {
           // lanes 0-15: gate of column 64 rank + 16 q + lane, lanes 16-31: up of the same columns
           const int c0 = 64 * (int)rank + 16 * q + (lane & 15), oc = t.n0 + c0;
@@ -451,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
               const float x = c + i < trows ? (float)v[i] * (rs[(c + i) & (kLightRows - 1)] * tn) : 0.f;
               const float up = __shfl_down_sync(0xffffffffu, x, 16);
               if (lane < 16 && c + i < trows && oc < p.N)
-                y[(int64_t)(t.row0 + c + i) * p.ldy + oc] = from_f32<Out>(silu_mul(x, up));
+                y[(int64_t)(t.row0 + c + i) * p.ldy + oc] = from_f32<Out>(silu_mul_fast(x, up));
             }
           }
         } else {
@@ -468,28 +557,54 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
           }
         }
       } else {
-        Out* const out = y + (int64_t)row * p.ldy + t.n0;
-#pragma unroll 1
-        for (int c = 0; c < kCols; c += 16) {
-          int g[16], u[16];
+        // 16 columns at a time; the next 16 leave TMEM while these are scaled and stored
+        const int row_first = t.row0 + 128 * (int)rank + q * 32, rows = t.row_end - row_first;
+        const int ncols = rows > 0 ? min(kCols, p.N - t.n0) : 0;
+        const float sr = m.row[slot][q * 32 + lane];
+        Out* const out = y + (int64_t)row_first * p.ldy + t.n0;
+        auto load = [&](int c, int (&g)[16], int (&u)[16]) {
           tmem_ld16i(tb + c, g);
           if (kSwiglu) tmem_ld16i(tb + kBN / 2 + c, u);
-          tmem_ld_wait();
-          const int left = p.N - t.n0 - c;
-          if (valid && left > 0) {
-            float v[16];
+        };
+        auto finish = [&](int c, const int (&g)[16], const int (&u)[16]) {
+          float v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              v[i] = (float)g[i] * (sr * col[c + i]);
-              if (kSwiglu) v[i] = silu_mul(v[i], (float)u[i] * (sr * col[kBN / 2 + c + i]));
+          for (int i = 0; i < 16; i += 4) {
+            const float4 tg = *reinterpret_cast<const float4*>(col + c + i);
+            const float tgs[4] = {tg.x, tg.y, tg.z, tg.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i + j] = (float)g[i + j] * (sr * tgs[j]);
+            if (kSwiglu) {
+              const float4 tu = *reinterpret_cast<const float4*>(col + kBN / 2 + c + i);
+              const float tus[4] = {tu.x, tu.y, tu.z, tu.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[i + j] = silu_mul_fast(v[i + j], (float)u[i + j] * (sr * tus[j]));
             }
-            store16(out + c, v, left, p.vec);
+          }
+          store_block(out + c, p.ldy, v, rows, ncols - c, p.vec, stage, lane);
+        };
+#pragma unroll 1
+        for (int c0 = 0; c0 < ncols; c0 += 64) {
+          int g[2][16], u[2][16];
+          load(c0, g[0], u[0]);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int c = c0 + 16 * b;
+            if (c < ncols) {
+              tmem_ld_wait16(g[b & 1]);
+              if (kSwiglu) tmem_ld_wait16(u[b & 1]);
+              if (b < 3 && c + 16 < ncols) load(c + 16, g[(b + 1) & 1], u[(b + 1) & 1]);
+              finish(c, g[b & 1], u[b & 1]);
+            }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&m.tempty[a]), 0));
+      if (lane == 0) {
+        mbar_arrive_cluster(mapa_shared(smem_u32(&m.tempty[a]), 0));
+        mbar_arrive(&m.pfree[slot]);
+      }
     }
   }
 
@@ -562,6 +677,8 @@ cudaError_t launch_pair(const IntGemmArgs& a, cudaStream_t s) {
   const int cols = kSwiglu ? kBN / 2 : kBN, osize = a.out_dtype == COLIBRI_BF16 ? 2 : 4;
   p.n_tiles = (a.N + cols - 1) / cols;
   p.vec = (a.ldy * osize) % 16 == 0;
+  // the token boxes of dense tiles and the transposes of unaligned rows share their memory
+  p.dense_rows = p.vec ? std::min(kDenseRows, p.light_rows) : 0;
   const long long bound = (long long)(a.rows / kBM + (a.offsets ? a.E : 1)) * p.n_tiles;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
