@@ -47,12 +47,13 @@ constexpr int kBN = 256;             // weight rows of a pair tile
 constexpr int kKB = 128;             // bytes of k per stage: one 128-byte swizzle atom
 constexpr int kHalf = 128 * kKB;     // 16 KB: this CTA's A or B part of a stage
 constexpr int kStage = 2 * kHalf;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kLightRows = 128;      // swapped tiles: at most 64 token rows per CTA
 constexpr int kDenseRows = 32;       // swapped tiles with two k blocks per stage
 constexpr int kTok = 16 * kKB;       // a 16-row box of token rows
 constexpr int kTmemCols = 512;
-constexpr int kStagePitch = 17;
+constexpr int kOutRow = 128;         // bytes of an output row that the epilogue gathers before it stores them
+constexpr int kOutPitch = kOutRow + 16;
 
 struct alignas(64) PairParams {
   CUtensorMap mapA, mapA16, mapA32, mapA64;  // rows, in boxes of 128, 16, 32 and 64
@@ -68,7 +69,6 @@ struct alignas(64) PairParams {
   int E, rows, N;
   int n_tiles, num_kb;
   int light_rows;  // m-tiles with at most this many rows run swapped (0: none)
-  int dense_rows;  // ... and with at most this many, two k blocks per stage
   bool vec;        // rows of y are 16-byte aligned
 };
 
@@ -94,11 +94,11 @@ struct PairSmem {
   Tile tile[kPlans];
   alignas(16) float col[kPlans][kBN];  // column scales of the tile (SwiGLU: gate | up)
   alignas(16) float row[kPlans][128];  // row scales: of this CTA's rows, or of a swapped tile's
+  alignas(16) uint8_t out[kEpiWarps][32 * kOutPitch];
 };
 constexpr size_t kPairTok = (size_t)kStages * 2 * kTok;
 constexpr size_t kPairSmem = (size_t)kStages * kStage + kPairTok + sizeof(PairSmem);
 static_assert(kPairSmem <= 232448, "shared memory of one CTA");
-static_assert(kEpiWarps * 32 * kStagePitch * 4 <= kPairTok, "transposes");
 
 // Group offsets (entry i counts as the largest of entries 0..i, within [0, rows]) and the m-tile
 // prefixes; one full warp.
@@ -253,40 +253,48 @@ __device__ __forceinline__ void tmem_ld_wait16(int (&v)[16]) {
 // silu(g) * u; the quotient by the approximate division (2 ulp)
 __device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// One warp: a block of 32 rows (lane = row) by 16 columns at `dst` (row 0, column 0), `rows` and `cols`
-// of which exist.  Rows that are 16-byte aligned and whole are written by their lanes; others are
-// transposed through shared memory so that the lanes write consecutive columns (a lane per row costs a
-// memory transaction per value: 32 us for the 256 x 256 tiles of an odd-width bf16 output, measured).
+// 16 values of this lane's row into the gathered block, at byte `at` of its 128.
 template <typename Out>
-__device__ __forceinline__ void store_block(Out* dst, int64_t ldy, const float (&v)[16], int rows, int cols, bool vec,
-                                            float* stage, int lane) {
-  if (vec && cols >= 16) {
-    if (lane < rows) {
-      Out* d = dst + lane * ldy;
-      if constexpr (sizeof(Out) == 2) {
-        uint32_t w[8];
+__device__ __forceinline__ void gather16(uint8_t* block, int lane, int at, const float (&v)[16]) {
+  uint4* d = reinterpret_cast<uint4*>(block + lane * kOutPitch + at);
+  if constexpr (sizeof(Out) == 2) {
+    uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          reinterpret_cast<float4*>(d)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    return;
-  }
+    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) stage[lane * kStagePitch + i] = v[i];
+    for (int i = 0; i < 4; ++i)
+      d[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                        __float_as_uint(v[4 * i + 3]));
+  }
+}
+
+// One warp: the gathered block of 32 rows by 128 bytes to `dst` (row 0, first column); `rows` and `cols`
+// of it exist.  Whole aligned rows go 8 lanes to a row, 128 contiguous bytes; others value by value,
+// the lanes on consecutive columns.  (Stores from the registers, a lane per row, touch 32 lines per
+// instruction: 3.3 us per 256 x 256 bf16 tile, 32 us where the rows are not aligned.)
+template <typename Out>
+__device__ __forceinline__ void store_block(Out* dst, int64_t ldy, const uint8_t* block, int rows, int cols, bool vec,
+                                            int lane) {
+  constexpr int kCols = kOutRow / (int)sizeof(Out);
   __syncwarp();
-  const int n = min(rows, 32), c = lane & 15;
-  if (c < cols) {
-#pragma unroll 4
-    for (int r = lane >> 4; r < n; r += 2) dst[r * ldy + c] = from_f32<Out>(stage[r * kStagePitch + c]);
+  const int n = min(rows, 32);
+  if (vec && cols >= kCols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const uint4 v = *reinterpret_cast<const uint4*>(block + r * kOutPitch + (lane & 7) * 16);
+      if (r < n) reinterpret_cast<uint4*>(dst + r * ldy)[lane & 7] = v;
+    }
+  } else {
+    for (int c = lane; c < min(cols, kCols); c += 32)
+#pragma unroll 8
+      for (int r = 0; r < n; ++r) dst[r * ldy + c] = reinterpret_cast<const Out*>(block + r * kOutPitch)[c];
   }
   __syncwarp();
 }
@@ -360,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
         const Tile t = m.tile[slot];
         mbar_arrive(&m.pfree[slot]);
         const int trows = t.row_end - t.row0;
-        const bool light = trows <= p.light_rows, dense = trows <= p.dense_rows;
+        const bool light = trows <= p.light_rows, dense = light && trows <= kDenseRows;
         const bool once = light && t.mtiles == 1;  // its weights are read by this tile alone: evict them first
         const int nh = (trows + 31) / 32 * 16;     // swapped: token rows (N / 2) per CTA
         const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
@@ -433,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(a * kBN);
         const int trows = t.row_end - t.row0;
-        const bool light = trows <= p.light_rows, dense = trows <= p.dense_rows;
+        const bool light = trows <= p.light_rows, dense = light && trows <= kDenseRows;
         const uint32_t idesc = light ? idesc_s8_s32(kBM, (trows + 31) / 32 * 32) : idesc_s8_s32(kBM, kBN);
         const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
         for (int step = 0; step < steps; ++step) {
@@ -507,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
   } else {
     // ------------------------------------------------------------- epilogue (warps 2..5, both CTAs)
     const int q = warp & 3;  // TMEM lane quarter this warp may access
-    float* stage = reinterpret_cast<float*>(tok_base) + q * (32 * kStagePitch);  // used when dense_rows is 0
+    uint8_t* block = m.out[q];
     Out* const y = static_cast<Out*>(p.y);
     int it = 0;
     for (int L = pair; L < total; L += npairs, ++it) {
@@ -581,22 +589,24 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
               for (int j = 0; j < 4; ++j) v[i + j] = silu_mul_fast(v[i + j], (float)u[i + j] * (sr * tus[j]));
             }
           }
-          store_block(out + c, p.ldy, v, rows, ncols - c, p.vec, stage, lane);
+          gather16<Out>(block, lane, c * (int)sizeof(Out) & (kOutRow - 1), v);
         };
+        constexpr int kBlocks = kOutRow / 16 / (int)sizeof(Out);  // of 16 columns, in a gathered block
 #pragma unroll 1
-        for (int c0 = 0; c0 < ncols; c0 += 64) {
+        for (int c0 = 0; c0 < ncols; c0 += 16 * kBlocks) {
           int g[2][16], u[2][16];
           load(c0, g[0], u[0]);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
+          for (int b = 0; b < kBlocks; ++b) {
             const int c = c0 + 16 * b;
             if (c < ncols) {
               tmem_ld_wait16(g[b & 1]);
               if (kSwiglu) tmem_ld_wait16(u[b & 1]);
-              if (b < 3 && c + 16 < ncols) load(c + 16, g[(b + 1) & 1], u[(b + 1) & 1]);
+              if (b + 1 < kBlocks && c + 16 < ncols) load(c + 16, g[(b + 1) & 1], u[(b + 1) & 1]);
               finish(c, g[b & 1], u[b & 1]);
             }
           }
+          store_block(out + c0, p.ldy, block, rows, ncols - c0, p.vec, lane);
         }
       }
       tc_fence_before();
@@ -677,8 +687,6 @@ cudaError_t launch_pair(const IntGemmArgs& a, cudaStream_t s) {
   const int cols = kSwiglu ? kBN / 2 : kBN, osize = a.out_dtype == COLIBRI_BF16 ? 2 : 4;
   p.n_tiles = (a.N + cols - 1) / cols;
   p.vec = (a.ldy * osize) % 16 == 0;
-  // the token boxes of dense tiles and the transposes of unaligned rows share their memory
-  p.dense_rows = p.vec ? std::min(kDenseRows, p.light_rows) : 0;
   const long long bound = (long long)(a.rows / kBM + (a.offsets ? a.E : 1)) * p.n_tiles;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
