@@ -405,6 +405,8 @@ struct IntGemmArgs {
   int out_dtype;           // COLIBRI_F32 or COLIBRI_BF16
   uint32_t* err;           // error word of bounded waits, or nullptr: the library's own word per device
 };
+constexpr int kSkinnyRows = 16;  // one group of at most this many rows: gemv_i8.cu
+cudaError_t launch_int_skinny(const IntGemmArgs& a, cudaStream_t s);
 cudaError_t int_gemm_take_error(uint32_t* word);  // reads and clears the current device's own word
 cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s);
 cudaError_t launch_quantize_rows(const void* x, int act, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,
@@ -606,6 +608,23 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     if (mbar_try_wait(bar, parity)) return true;
     if ((++n & 255u) == 0 && global_ns() - t0 > kWaitTimeoutNs) return false;
   }
+}
+
+// ---------------------------------------------------------------------------------------
+// Rings in shared memory that a lane fills and drains by itself
+// ---------------------------------------------------------------------------------------
+// 16 bytes, past L1, fetching the 256 bytes around them into L2 (a warp walks along its rows)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
 }
 
 // ---------------------------------------------------------------------------------------

@@ -8,14 +8,14 @@
 // fp32 and the two scales round once each, and the result once to its type.
 //
 // i8_pair_kernel: clusters of two CTAs (tcgen05 cta_group::2, kind::i8), persistent, one pair per two
-// SMs, 224 threads per CTA:
+// SMs, 352 threads per CTA:
 //   warp 0      TMA producer: this CTA's 128 rows of A and 128 of the 256 weight rows of the tile
 //               (SwiGLU: the leader W1, the peer W3), 128 bytes of k per stage, into a ring of 32 KB
 //               stages; both CTAs' copies count on the leader's barrier.
 //   warp 1      the leader issues the M = 256, N = 256, K = 32 MMAs, four per stage, into one of two
 //               accumulators (128 rows x 256 int32 columns of TMEM in each CTA).
-//   warps 2-5   epilogue: TMEM -> registers, scales, SwiGLU, stores; it overlaps the next tile's MMAs.
-//   warp 6      planner: finds the tiles ahead of the other roles and fetches their scales (done by the
+//   warps 2-9   epilogue: TMEM -> registers, scales, SwiGLU, stores; it overlaps the next tile's MMAs.
+//   warp 10     planner: finds the tiles ahead of the other roles and fetches their scales (done by the
 //               roles themselves this cost 1.5 us between two tiles of MMAs and 3 us per epilogue)
 // A group's last m-tile of at most 128 rows runs with the operands swapped (weights the M side, its
 // rows rounded up to 32 the N side), so that a group of a few rows costs the stream of its weights
@@ -37,8 +37,8 @@ namespace {
 // Set by a bounded wait that gave up, when the caller brings no word of its own.
 __device__ uint32_t g_int_err;
 
-// (two warps per quarter of the TMEM lanes measured slower: expert gate/up 788 against 730 us)
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;          // two per quarter of the TMEM lanes (one: fine-grained down 96 against 92 us)
+constexpr int kEpiHalves = kEpiWarps / 4;
 constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = 96 + kEpiThreads;
 constexpr int kPlans = 4;            // tiles the planner may be ahead
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
       mbar_wait_bounded(&m.drain, 0);
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == 2 + kEpiWarps) {
     // ------------------------------------------------------------- planner (both CTAs)
     int it = 0;
     for (int L = pair; L < total; L += npairs, ++it) {
@@ -513,9 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
       if (lane == 0) mbar_arrive(&m.sfull[slot]);
     }
   } else {
-    // ------------------------------------------------------------- epilogue (warps 2..5, both CTAs)
+    // ------------------------------------------------------------- epilogue (warps 2..9, both CTAs)
     const int q = warp & 3;  // TMEM lane quarter this warp may access
-    uint8_t* block = m.out[q];
+    const int half = (warp - 2) >> 2;  // the quarter's two warps take alternate blocks
+    uint8_t* block = m.out[warp - 2];
     Out* const y = static_cast<Out*>(p.y);
     int it = 0;
     for (int L = pair; L < total; L += npairs, ++it) {
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
           // lanes 0-15: gate of column 64 rank + 16 q + lane, lanes 16-31: up of the same columns
           const int c0 = 64 * (int)rank + 16 * q + (lane & 15), oc = t.n0 + c0;
           const float tn = col[(lane < 16 ? 0 : kBN / 2) + c0];
-          for (int c = 0; c < trows; c += 16) {
+          for (int c = 16 * half; c < trows; c += 16 * kEpiHalves) {
             int v[16];
             tmem_ld16i(tb + c, v);
             tmem_ld_wait();
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
         } else {
           const int c0 = 128 * (int)rank + q * 32 + lane, oc = t.n0 + c0;
           const float tn = col[c0];
-          for (int c = 0; c < trows; c += 16) {
+          for (int c = 16 * half; c < trows; c += 16 * kEpiHalves) {
             int v[16];
             tmem_ld16i(tb + c, v);
             tmem_ld_wait();
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
         };
         constexpr int kBlocks = kOutRow / 16 / (int)sizeof(Out);  // of 16 columns, in a gathered block
 #pragma unroll 1
-        for (int c0 = 0; c0 < ncols; c0 += 16 * kBlocks) {
+        for (int c0 = 16 * kBlocks * half; c0 < ncols; c0 += 16 * kBlocks * kEpiHalves) {
           int g[2][16], u[2][16];
           load(c0, g[0], u[0]);
 #pragma unroll
@@ -703,6 +704,7 @@ cudaError_t launch_pair(const IntGemmArgs& a, cudaStream_t s) {
 
 cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s) {
   if (a.rows <= 0) return cudaSuccess;
+  if (!swiglu && !a.offsets && a.rows <= kSkinnyRows) return launch_int_skinny(a, s);
   return swiglu ? launch_pair<true>(a, s) : launch_pair<false>(a, s);
 }
 
