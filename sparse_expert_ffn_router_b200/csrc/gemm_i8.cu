@@ -25,6 +25,14 @@
 // Tiles are numbered group-major, then n-tile, then m-tile fastest, so that the pairs running together
 // share weight tiles through L2; groups of a single m-tile (streams of weights) are interleaved with
 // the others in proportion.  Pair i takes tiles i, i + pairs, ...
+//
+// i8_split_kernel: products of too few pair tiles to occupy the GPU.  Tiles of 128 x 128 (one CTA each,
+// cta_group::1) whose k range is split over the S = 1, 2 or 4 CTAs of a cluster; the int32 partial
+// sums, exact in any order, are exchanged through the cluster's shared memory (the idle ring), each
+// CTA finishing 1 / S of the columns.  What bounds such a product is the feed of one SM's shared
+// memory (about 100 GB/s measured, against 43 GB/s of HBM per SM), so the SMs left idle are worth more
+// than the larger tile: 4096 x 4096 at 128 rows 19.4 us as pair tiles.
+//
 // Every wait is bounded (kWaitTimeoutNs); one that gives up sets the error word and ends all roles.
 #include <algorithm>
 #include <cstring>
@@ -77,6 +85,7 @@ struct Tile {
 };
 
 struct PairSmem {
+  static constexpr bool kClasses = true;  // tiles of groups with one m-tile are interleaved with the others
   uint64_t full[kStages];   // used in the leader: both CTAs' copies
   uint64_t empty[kStages];  // per CTA: freed by the leader's multicast commit
   uint64_t tfull[2];        // per CTA: accumulator ready (multicast commit)
@@ -101,19 +110,20 @@ constexpr size_t kPairSmem = (size_t)kStages * kStage + kPairTok + sizeof(PairSm
 static_assert(kPairSmem <= 232448, "shared memory of one CTA");
 
 // Group offsets (entry i counts as the largest of entries 0..i, within [0, rows]) and the m-tile
-// prefixes; one full warp.
-__device__ void pair_schedule(PairSmem& m, const PairParams& p) {
+// prefixes for tiles of kRows rows; one full warp.
+template <int kRows, typename Smem>
+__device__ void schedule(Smem& m, const int32_t* offsets, int E, int rows) {
   const int lane = threadIdx.x & 31;
   constexpr int kPer = kMaxExperts / 32;
-  const int per = (p.E + 31) / 32, e0 = lane * per;  // this lane's groups
+  const int per = (E + 31) / 32, e0 = lane * per;  // this lane's groups
   int end[kPer];                                     // entry e0 + i + 1
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     end[i] = 0;
-    if (i < per && e0 + i < p.E) end[i] = p.offsets ? min(max(p.offsets[e0 + i + 1], 0), p.rows) : p.rows;
+    if (i < per && e0 + i < E) end[i] = offsets ? min(max(offsets[e0 + i + 1], 0), rows) : rows;
   }
   int first = 0;
-  if (lane == 0 && p.offsets) first = min(max(p.offsets[0], 0), p.rows);
+  if (lane == 0 && offsets) first = min(max(offsets[0], 0), rows);
   int top = first;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) top = max(top, end[i]);
@@ -128,8 +138,8 @@ __device__ void pair_schedule(PairSmem& m, const PairParams& p) {
   int at = begin;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (i < per && e0 + i < p.E) {
-      const int to = max(at, end[i]), mt = (to - at + kBM - 1) / kBM;
+    if (i < per && e0 + i < E) {
+      const int to = max(at, end[i]), mt = (to - at + kRows - 1) / kRows;
       end[i] = to;
       all += mt;
       heavy += mt >= 2 ? mt : 0;
@@ -149,19 +159,22 @@ __device__ void pair_schedule(PairSmem& m, const PairParams& p) {
   heavy = ih - heavy;
   if (lane == 0) {
     m.off[0] = first;
-    m.mt[0] = m.hv[0] = m.lt[0] = 0;
+    m.mt[0] = 0;
+    if constexpr (Smem::kClasses) m.hv[0] = m.lt[0] = 0;
   }
   at = begin;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if (i < per && e0 + i < p.E) {
-      const int mt = (end[i] - at + kBM - 1) / kBM;
+    if (i < per && e0 + i < E) {
+      const int mt = (end[i] - at + kRows - 1) / kRows;
       all += mt;
       heavy += mt >= 2 ? mt : 0;
       m.off[e0 + i + 1] = end[i];
       m.mt[e0 + i + 1] = all;
-      m.hv[e0 + i + 1] = heavy;
-      m.lt[e0 + i + 1] = all - heavy;  // a group has one m-tile, or is heavy, or is empty
+      if constexpr (Smem::kClasses) {
+        m.hv[e0 + i + 1] = heavy;
+        m.lt[e0 + i + 1] = all - heavy;  // a group has one m-tile, or is heavy, or is empty
+      }
       at = end[i];
     }
   }
@@ -344,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
     tmem_relinquish_pair();
     tc_fence_before();
   }
-  if (warp == 0) pair_schedule(m, p);
+  if (warp == 0) schedule<kBM>(m, p.offsets, p.E, p.rows);
   __syncthreads();
   cluster_sync_all();  // the peer's barriers are initialised before any cross-CTA arrival
   tc_fence_after();
@@ -633,47 +646,246 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
   }
 }
 
+// ------------------------------------------------------------------------- split kernel
+constexpr int kSplitTile = 128;    // rows and weight rows of a tile
+constexpr int kSplitStages = 6;
+constexpr int kSplitThreads = 192;  // producer, MMA, four epilogue warps
+constexpr int kSplitMax = 4;
+constexpr int kSplitTmem = 128;
+
+struct alignas(64) SplitParams {
+  CUtensorMap mapA;  // rows, boxes of 128
+  CUtensorMap mapB;  // weights, boxes of 128 rows (SwiGLU: 64)
+  const int32_t* offsets;
+  const float* a_scale;
+  const float* w_scale;
+  int64_t s_stride;
+  void* y;
+  int64_t ldy;
+  uint32_t* err;
+  int E, rows, N;
+  int n_tiles, num_kb, split;
+  bool vec;
+};
+
+struct SplitSmem {
+  static constexpr bool kClasses = false;
+  uint64_t full[kSplitStages];
+  uint64_t empty[kSplitStages];
+  uint64_t tfull;
+  uint32_t tmem_base;
+  int abort;
+  int issued, consumed;
+  int32_t off[kMaxExperts + 1];
+  int32_t mt[kMaxExperts + 1];
+  alignas(16) float col[kSplitTile];
+  alignas(16) float row[kSplitTile];
+  alignas(16) uint8_t out[4][32 * kOutPitch];
+};
+constexpr size_t kSplitSmem = (size_t)kSplitStages * kStage + sizeof(SplitSmem);
+static_assert(kSplitSmem <= 232448, "shared memory of one CTA");
+// partial sums received: [source][16-byte unit of 4 columns][row]
+static_assert((size_t)kSplitMax * kSplitTile * kSplitTile / kSplitMax * 4 <= (size_t)kSplitStages * kStage, "exchange");
+
+__device__ __forceinline__ void st_shared_cluster_v4(uint32_t cluster_addr, int a, int b, int c, int d) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+template <bool kSwiglu, typename Out>
+__global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid_constant__ SplitParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint32_t* err = p.err ? p.err : &g_int_err;
+  SplitSmem& m = *reinterpret_cast<SplitSmem*>(smem + (size_t)kSplitStages * kStage);
+  volatile int* abort_flag = &m.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.split, rank = S > 1 ? (int)cluster_ctarank() : 0;
+  constexpr int kCols = kSwiglu ? kSplitTile / 2 : kSplitTile;  // output columns of a tile
+  const bool aligned = (smem_u32(smem) & 1023u) == 0;  // needed by the 128-byte swizzle; the same in every CTA
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSplitStages; ++s) {
+      mbar_init(&m.full[s], 1);
+      mbar_init(&m.empty[s], 1);
+    }
+    mbar_init(&m.tfull, 1);
+    m.abort = 0;
+    m.issued = m.consumed = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&p.mapA);
+    tma_prefetch_desc(&p.mapB);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 1) {
+    tmem_alloc(&m.tmem_base, kSplitTmem);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  if (warp == 0) schedule<kSplitTile>(m, p.offsets, p.E, p.rows);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = m.tmem_base;
+
+  // the tile: group-major, then n, then m
+  const int L = (int)blockIdx.x / S;
+  const bool work = aligned && L < m.mt[p.E] * p.n_tiles;  // the same in every CTA of the cluster
+  Tile t = {0, 0, 0, 0, 1};
+  if (work) {
+    t.e = find_group(m.mt, p.E, p.n_tiles, L);
+    t.mtiles = m.mt[t.e + 1] - m.mt[t.e];
+    const int r = L - m.mt[t.e] * p.n_tiles, n = r / t.mtiles;
+    t.row0 = m.off[t.e] + (r - n * t.mtiles) * kSplitTile;
+    t.row_end = m.off[t.e + 1];
+    t.n0 = n * kCols;
+  } else if (!aligned && threadIdx.x == 0) {
+    atomicOr(err, kErrWaitTimeout);
+  }
+  const int kb0 = p.num_kb * rank / S, kb1 = p.num_kb * (rank + 1) / S;  // this CTA's k blocks
+
+  if (work && warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+        const int s = issued % kSplitStages;
+        if (!wait_or_abort(&m.empty[s], ((uint32_t)(issued / kSplitStages) & 1u) ^ 1u, abort_flag)) {
+          raise_abort(m, err);
+          break;
+        }
+        uint8_t* sA = smem + (size_t)s * kStage;
+        uint8_t* sB = sA + kHalf;
+        mbar_arrive_expect_tx(&m.full[s], kStage);
+        tma_load_2d(sA, &p.mapA, &m.full[s], kb * kKB, t.row0);
+        if (kSwiglu) {
+          tma_load_4d(sB, &p.mapB, &m.full[s], kb * kKB, t.n0, 0, t.e);
+          tma_load_4d(sB + kHalf / 2, &p.mapB, &m.full[s], kb * kKB, t.n0, 1, t.e);
+        } else {
+          tma_load_3d(sB, &p.mapB, &m.full[s], kb * kKB, t.n0, t.e);
+        }
+      }
+      m.issued = issued;
+    }
+    __syncwarp();
+  } else if (work && warp == 1) {
+    if (lane == 0) {
+      int consumed = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++consumed) {
+        const int s = consumed % kSplitStages;
+        if (!wait_or_abort(&m.full[s], (uint32_t)(consumed / kSplitStages) & 1u, abort_flag)) {
+          raise_abort(m, err);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sA = smem_u32(smem + (size_t)s * kStage);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_i8(tmem_base, smem_desc_sw128(sA + kk * 32), smem_desc_sw128(sA + kHalf + kk * 32),
+                    idesc_s8_s32(kSplitTile, kSplitTile), (consumed | kk) != 0 ? 1u : 0u);
+        tc_commit(&m.empty[s]);
+      }
+      m.consumed = consumed;
+      tc_commit(&m.tfull);  // also after an error: every MMA issued has ended
+      mbar_wait_bounded(&m.tfull, 0);
+    }
+    __syncwarp();
+  } else if (work && warp >= 2) {
+    // the tile's scales, while the products run
+    const int i = threadIdx.x - 64;
+    const float* ws = p.w_scale + (size_t)t.e * p.s_stride;
+    const int n = t.n0 + (kSwiglu ? i & (kCols - 1) : i);
+    m.col[i] = n < p.N ? __ldg(ws + (kSwiglu && i >= kCols ? p.N : 0) + n) : 0.f;
+    m.row[i] = t.row0 + i < t.row_end ? __ldg(p.a_scale + t.row0 + i) : 0.f;
+  }
+  __syncthreads();  // this CTA's products have ended: its ring is idle
+  if (threadIdx.x == 0 && m.abort)
+    for (int i = m.consumed; i < m.issued; ++i)  // error path: copies that no product waited for
+      mbar_wait_bounded(&m.full[i % kSplitStages], (uint32_t)(i / kSplitStages) & 1u);
+  __syncthreads();
+  const bool ok = work && !m.abort;
+  tc_fence_after();
+
+  // columns of the tile that this CTA finishes: 1 / S of them (SwiGLU: of the gate and of the up columns)
+  const int own = kCols / S;
+  const int q = warp & 3;
+  const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
+  constexpr int kParts = kSwiglu ? 2 : 1;
+  const int units = own * kParts / 4;  // 16-byte units of 4 columns per source and row
+  if (S > 1) {
+    cluster_sync_all();  // the rings of all CTAs are idle
+    if (ok && warp >= 2) {
+      const int row = q * 32 + lane;
+      for (int j = 1; j < S; ++j) {
+        const int to = (rank + j) % S;
+        for (int part = 0; part < kParts; ++part)
+          for (int c = 0; c < own; c += 16) {
+            int v[16];
+            tmem_ld16i(tb + part * kCols + to * own + c, v);
+            tmem_ld_wait16(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int unit = rank * units + (part * own + c) / 4 + i;
+              st_shared_cluster_v4(mapa_shared(smem_u32(smem) + (uint32_t)(unit * kSplitTile + row) * 16u, (uint32_t)to),
+                                   v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+          }
+      }
+    }
+    cluster_sync_all();  // the partial sums have arrived
+  }
+  if (ok && warp >= 2) {
+    const int row_first = t.row0 + q * 32, rows = t.row_end - row_first, c_first = rank * own;
+    const int ncols = rows > 0 ? min(own, p.N - t.n0 - c_first) : 0;
+    const float sr = m.row[q * 32 + lane];
+    Out* const out = static_cast<Out*>(p.y) + (int64_t)row_first * p.ldy + t.n0 + c_first;
+    constexpr int kBlock = kOutRow / (int)sizeof(Out);  // columns of a gathered block
+    auto sums = [&](int part, int c, int (&v)[16]) {
+      tmem_ld16i(tb + part * kCols + c_first + c, v);
+      tmem_ld_wait16(v);
+      for (int j = 1; j < S; ++j) {
+        const int from = (rank + j) % S;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int unit = from * units + (part * own + c) / 4 + i;
+          const int4 w = *reinterpret_cast<const int4*>(smem + (size_t)(unit * kSplitTile + q * 32 + lane) * 16);
+          v[4 * i] += w.x;
+          v[4 * i + 1] += w.y;
+          v[4 * i + 2] += w.z;
+          v[4 * i + 3] += w.w;
+        }
+      }
+    };
+    for (int c = 0; c < ncols; c += 16) {
+      int g[16], u[16];
+      sums(0, c, g);
+      if (kSwiglu) sums(1, c, u);
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[i] = (float)g[i] * (sr * m.col[c_first + c + i]);
+        if (kSwiglu) v[i] = silu_mul_fast(v[i], (float)u[i] * (sr * m.col[kCols + c_first + c + i]));
+      }
+      gather16<Out>(m.out[q], lane, c * (int)sizeof(Out) & (kOutRow - 1), v);
+      const int at = c & ~(kBlock - 1);  // the block's first column
+      if (c + 16 >= ncols || c + 16 - at == kBlock)
+        store_block(out + at, p.ldy, m.out[q], rows, ncols - at, p.vec, lane);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kSplitTmem);
+  }
+}
+
 bool byte_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
               const uint32_t* box) {
   return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides, box);
 }
 
-template <bool kSwiglu>
-cudaError_t launch_pair(const IntGemmArgs& a, cudaStream_t s) {
-  PairParams p;
-  memset(&p, 0, sizeof(p));
-  const uint64_t K = a.K, N = a.N, E = a.E;
-  const uint64_t es = a.w_stride > 0 ? (uint64_t)a.w_stride : (uint64_t)a.ldw;  // a single group: not used
-  bool ok = true;
-  {
-    uint64_t dims[2] = {K, (uint64_t)a.rows}, st[1] = {(uint64_t)a.lda};
-    uint32_t box[2] = {kKB, 128};
-    ok &= byte_map(&p.mapA, a.A, 2, dims, st, box);
-    box[1] = 16;
-    ok &= byte_map(&p.mapA16, a.A, 2, dims, st, box);
-    box[1] = 32;
-    ok &= byte_map(&p.mapA32, a.A, 2, dims, st, box);
-    box[1] = 64;
-    ok &= byte_map(&p.mapA64, a.A, 2, dims, st, box);
-  }
-  p.light_rows = kLightRows;
-  if (kSwiglu) {
-    uint64_t dims[4] = {K, N, 2, E}, st[3] = {K, N * K, es};
-    uint32_t box[4] = {kKB, 128, 1, 1};
-    ok &= byte_map(&p.mapB, a.W, 4, dims, st, box);
-    if (N % 16 == 0) {
-      uint64_t dims16[5] = {K, 16, 2, N / 16, E}, st16[4] = {K, N * K, 16 * K, es};
-      uint32_t box16[5] = {kKB, 16, 2, 4, 1};
-      ok &= byte_map(&p.mapB16, a.W, 5, dims16, st16, box16);
-    } else {
-      p.light_rows = 0;
-    }
-  } else {
-    uint64_t dims[3] = {K, N, E}, st[2] = {(uint64_t)a.ldw, es};
-    uint32_t box[3] = {kKB, 128, 1};
-    ok &= byte_map(&p.mapB, a.W, 3, dims, st, box);
-  }
-  if (!ok) return cudaErrorInvalidValue;
+// What both kernels are told.
+template <typename Params>
+void fill_params(Params& p, const IntGemmArgs& a, int tile_cols) {
   p.offsets = a.offsets;
   p.a_scale = a.a_scale;
   p.w_scale = a.w_scale;
@@ -685,19 +897,74 @@ cudaError_t launch_pair(const IntGemmArgs& a, cudaStream_t s) {
   p.rows = a.rows;
   p.N = a.N;
   p.num_kb = (a.K + kKB - 1) / kKB;
-  const int cols = kSwiglu ? kBN / 2 : kBN, osize = a.out_dtype == COLIBRI_BF16 ? 2 : 4;
-  p.n_tiles = (a.N + cols - 1) / cols;
-  p.vec = (a.ldy * osize) % 16 == 0;
+  p.n_tiles = (a.N + tile_cols - 1) / tile_cols;
+  p.vec = (a.ldy * (a.out_dtype == COLIBRI_BF16 ? 2 : 4)) % 16 == 0;
+}
+
+// Weights as [K, N, E], or for SwiGLU [K, N, W1 | W3, E], in boxes of `rows` weight rows.
+bool weight_map(CUtensorMap* map, const IntGemmArgs& a, bool swiglu, uint32_t rows) {
+  const uint64_t K = a.K, N = a.N, E = a.E;
+  const uint64_t es = a.w_stride > 0 ? (uint64_t)a.w_stride : (uint64_t)a.ldw;  // a single group: not used
+  if (swiglu) {
+    uint64_t dims[4] = {K, N, 2, E}, st[3] = {K, N * K, es};
+    uint32_t box[4] = {kKB, rows, 1, 1};
+    return byte_map(map, a.W, 4, dims, st, box);
+  }
+  uint64_t dims[3] = {K, N, E}, st[2] = {(uint64_t)a.ldw, es};
+  uint32_t box[3] = {kKB, rows, 1};
+  return byte_map(map, a.W, 3, dims, st, box);
+}
+
+bool row_map(CUtensorMap* map, const IntGemmArgs& a, uint32_t rows) {
+  uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)a.rows}, st[1] = {(uint64_t)a.lda};
+  uint32_t box[2] = {kKB, rows};
+  return byte_map(map, a.A, 2, dims, st, box);
+}
+
+template <typename Kernel, typename Params>
+cudaError_t launch_configured(Kernel kern, unsigned grid, int threads, size_t smem, unsigned cluster, const Params& p,
+                              cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  return e != cudaSuccess ? e : launch_kernel(kern, dim3(grid), dim3(threads), smem, s, cluster, p);
+}
+
+template <bool kSwiglu>
+cudaError_t launch_pair(const IntGemmArgs& a, int sms, cudaStream_t s) {
+  PairParams p;
+  memset(&p, 0, sizeof(p));
+  constexpr int cols = kSwiglu ? kBN / 2 : kBN;
+  fill_params(p, a, cols);
+  bool ok = row_map(&p.mapA, a, 128) && row_map(&p.mapA16, a, 16) && row_map(&p.mapA32, a, 32) &&
+            row_map(&p.mapA64, a, 64) && weight_map(&p.mapB, a, kSwiglu, 128);
+  p.light_rows = kLightRows;
+  if (kSwiglu) {
+    const uint64_t K = a.K, N = a.N;
+    if (N % 16 == 0) {
+      uint64_t dims[5] = {K, 16, 2, N / 16, (uint64_t)a.E}, st[4] = {K, N * K, 16 * K, (uint64_t)a.w_stride};
+      uint32_t box[5] = {kKB, 16, 2, 4, 1};
+      ok = ok && byte_map(&p.mapB16, a.W, 5, dims, st, box);
+    } else {
+      p.light_rows = 0;
+    }
+  }
+  if (!ok) return cudaErrorInvalidValue;
   const long long bound = (long long)(a.rows / kBM + (a.offsets ? a.E : 1)) * p.n_tiles;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   const unsigned pairs = (unsigned)std::min<long long>(bound, sms / 2);
   auto kern = a.out_dtype == COLIBRI_BF16 ? i8_pair_kernel<kSwiglu, __nv_bfloat16> : i8_pair_kernel<kSwiglu, float>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(2 * pairs), dim3(kThreads), kPairSmem, s, 2, p);
+  return launch_configured(kern, 2 * pairs, kThreads, kPairSmem, 2, p, s);
+}
+
+// `tiles`: how many 128 x 128 tiles there may be; each on `split` CTAs.
+template <bool kSwiglu>
+cudaError_t launch_split(const IntGemmArgs& a, int tiles, int split, cudaStream_t s) {
+  SplitParams p;
+  memset(&p, 0, sizeof(p));
+  fill_params(p, a, kSwiglu ? kSplitTile / 2 : kSplitTile);
+  if (!row_map(&p.mapA, a, kSplitTile) || !weight_map(&p.mapB, a, kSwiglu, kSwiglu ? kSplitTile / 2 : kSplitTile))
+    return cudaErrorInvalidValue;
+  p.split = split;
+  auto kern = a.out_dtype == COLIBRI_BF16 ? i8_split_kernel<kSwiglu, __nv_bfloat16> : i8_split_kernel<kSwiglu, float>;
+  return launch_configured(kern, (unsigned)(tiles * split), kSplitThreads, kSplitSmem, (unsigned)split, p, s);
 }
 
 }  // namespace
@@ -705,7 +972,22 @@ cudaError_t launch_pair(const IntGemmArgs& a, cudaStream_t s) {
 cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s) {
   if (a.rows <= 0) return cudaSuccess;
   if (!swiglu && !a.offsets && a.rows <= kSkinnyRows) return launch_int_skinny(a, s);
-  return swiglu ? launch_pair<true>(a, s) : launch_pair<false>(a, s);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // Fewer tiles of 128 x 128 than SMs: one CTA per tile, or with k split 2 or 4 CTAs, all at once;
+  // more tiles keep the pair kernel's SMs busy.
+  const int groups = a.offsets ? a.E : 1, cols = swiglu ? kSplitTile / 2 : kSplitTile;
+  const long long tiles = (a.offsets ? (long long)a.rows / kSplitTile + groups : (a.rows + kSplitTile - 1) / kSplitTile) *
+                          ((a.N + cols - 1) / cols);
+  if (tiles <= sms) {
+    const int kbs = (a.K + kKB - 1) / kKB;
+    int split = 1;
+    while (split < kSplitMax && tiles * split * 2 <= sms && kbs >= 4 * split) split *= 2;
+    return swiglu ? launch_split<true>(a, (int)tiles, split, s) : launch_split<false>(a, (int)tiles, split, s);
+  }
+  return swiglu ? launch_pair<true>(a, sms, s) : launch_pair<false>(a, sms, s);
 }
 
 // The error word of calls without one of their own, read and cleared (after `s` is idle).
