@@ -49,7 +49,13 @@ typedef enum {
   COLIBRI_ERR_TIMEOUT = -6      /* a device-side wait gave up (reported by colibri_sync_status) */
 } colibri_status;
 
-typedef enum { COLIBRI_F32 = 0, COLIBRI_BF16 = 1, COLIBRI_I8 = 2, COLIBRI_I4 = 3 } colibri_dtype;
+typedef enum {
+  COLIBRI_F32 = 0,
+  COLIBRI_BF16 = 1,
+  COLIBRI_I8 = 2,
+  COLIBRI_I4 = 3,
+  COLIBRI_I8A8 = 4 /* weight_dtype only: COLIBRI_I8 weights, multiplied with activations rounded to int8 */
+} colibri_dtype;
 
 /* Layout of the int8 weight scales (colibri_desc.weight_scale_mode). */
 typedef enum {
@@ -88,6 +94,12 @@ typedef enum {
  *                                (www.mhpq.cn/news/563172 §4.2: INT4 packed in INT32, group
  *                                size 128; www.trdm.cn/news/555962 §6.1: two 4-bit weights per
  *                                byte); d_model and d_ff multiples of 128.
+ *                   (BF16, I8A8) the weights and per-channel scales of (BF16, I8), with the
+ *                   activations rounded to int8 too: x and, between the projections, H (kept in
+ *                   bf16 before that) get one scale per row as in colibri_quantize_rows, and both
+ *                   projections run once on the int8 tensor cores (about twice the bf16 rate).
+ *                   Meant for prefill, where (BF16, I8), which keeps activations at 15 bits in two
+ *                   planes, streams the weights again for every 32 tokens.  d_ff <= 131056.
  *                   The shared expert is available for (F32, F32) and (BF16, BF16).
  *   max_tokens      largest T a forward may be called with (sizes the workspace).
  *   device_id       CUDA device the context lives on.
@@ -147,7 +159,7 @@ int64_t colibri_expert_stride(const colibri_ctx* ctx);
  *   expert_w     device; expert e starts at element e * colibri_expert_stride(ctx) and holds
  *                W1[f][d] | W3[f][d] | W2[d][f], each row-major with rows = output channels
  *                ([out, in]).  W1 is the gate, W3 the up and W2 the down projection.
- *   expert_scales  COLIBRI_I8: device fp32, per expert e at e * (2f + d): s1[f] | s3[f] |
+ *   expert_scales  COLIBRI_I8 and COLIBRI_I8A8: device fp32, per expert e at e * (2f + d): s1[f] | s3[f] |
  *                s2[d]; weight W[o][i] = s[o] * q[o][i] (with COLIBRI_SCALE_PER_MATRIX: at 3 * e,
  *                s1 | s3 | s2, W[o][i] = s * q[o][i]).
  *                COLIBRI_I4: device fp32, per expert e at e * 3 * d * f / 128: s1[d/128][f] |
@@ -203,8 +215,8 @@ colibri_status colibri_moe_forward_routed(colibri_ctx* ctx, const void* x, int32
  * time counts as the gate/up stage) are those of colibri_moe_forward.  The two entry points agree
  * within the rounding of their sums, not bit for bit; a call's result does not vary from run to
  * run.  The launch needs every SM of the device for a CTA of 512 threads: beside other work it
- * starts once they are free.  Errors: INVALID_ARG (also T > 16), ALIGNMENT, UNSUPPORTED (int8 and
- * int4 weights, which colibri_moe_forward streams at these sizes), CUDA.
+ * starts once they are free.  Errors: INVALID_ARG (also T > 16), ALIGNMENT, UNSUPPORTED
+ * (quantised weights, which colibri_moe_forward streams at these sizes), CUDA.
  */
 colibri_status colibri_moe_decode(colibri_ctx* ctx, const void* x, int32_t T,
                                   const void* router_w, const float* router_b,

@@ -16,7 +16,7 @@ from typing import Optional
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcolibri.so")
 
-COLIBRI_F32, COLIBRI_BF16, COLIBRI_I8, COLIBRI_I4 = 0, 1, 2, 3
+COLIBRI_F32, COLIBRI_BF16, COLIBRI_I8, COLIBRI_I4, COLIBRI_I8A8 = 0, 1, 2, 3, 4
 COLIBRI_ROUTER_CLAMP, COLIBRI_ROUTER_RAW_WEIGHTS = 1, 2
 COLIBRI_SCALE_PER_CHANNEL, COLIBRI_SCALE_PER_MATRIX = 0, 1
 

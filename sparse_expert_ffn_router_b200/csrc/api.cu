@@ -167,15 +167,18 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   const bool bf16 = D.act_dtype == COLIBRI_BF16 && D.weight_dtype == COLIBRI_BF16;
   const bool w8 = D.act_dtype == COLIBRI_BF16 && D.weight_dtype == COLIBRI_I8;
   const bool w4 = D.act_dtype == COLIBRI_BF16 && D.weight_dtype == COLIBRI_I4;
+  const bool w8a8 = D.act_dtype == COLIBRI_BF16 && D.weight_dtype == COLIBRI_I8A8;
   const bool i8 = w8 || w4;  // the weight-streaming path (int8 tensor cores over activation planes)
-  if (D.act_dtype < 0 || D.act_dtype > 2 || D.weight_dtype < 0 || D.weight_dtype > 3)
+  if (D.act_dtype < 0 || D.act_dtype > 2 || D.weight_dtype < 0 || D.weight_dtype > 4)
     return fail(nullptr, COLIBRI_ERR_INVALID_ARG, "unknown dtype code (act=%d, weight=%d)", D.act_dtype, D.weight_dtype);
-  if (!f32 && !bf16 && !i8)
+  if (!f32 && !bf16 && !i8 && !w8a8)
     return fail(nullptr, COLIBRI_ERR_UNSUPPORTED, "dtype pair (act=%d, weight=%d) not supported", D.act_dtype, D.weight_dtype);
-  if (i8 && D.shared_d_ff > 0)
+  if ((i8 || w8a8) && D.shared_d_ff > 0)
     return fail(nullptr, COLIBRI_ERR_UNSUPPORTED, "shared expert with int8 / int4 weights is not supported");
   if (i8 && D.d_ff > kDecMaxFF)
     return fail(nullptr, COLIBRI_ERR_UNSUPPORTED, "int8 / int4 weights support d_ff <= %d", kDecMaxFF);
+  if (w8a8 && D.d_ff > kIntMaxK)
+    return fail(nullptr, COLIBRI_ERR_UNSUPPORTED, "int8 products support d_ff <= %d", kIntMaxK);
   if (w4 && (D.d_model % 128 != 0 || D.d_ff % 128 != 0))
     return fail(nullptr, COLIBRI_ERR_INVALID_ARG, "int4 weights need d_model and d_ff multiples of 128 (the scale group)");
   if (!w8 && D.weight_scale_mode != COLIBRI_SCALE_PER_CHANNEL)
@@ -219,7 +222,7 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   const size_t o_idx = c.take(R * 4), o_w = c.take(R * 4), o_dst = c.take(R * 4), o_src = c.take(R * 4);
   const size_t o_bc = c.take((size_t)nblk * E * 4), o_bb = c.take((size_t)nblk * E * 4);
   const size_t o_cnt = c.take(E * 4), o_off = c.take((E + 1) * 4), o_mt = c.take((E + 1) * 4);
-  const size_t o_xp = c.take(i8 ? 0 : R * d * as);  // int8 weights read the row planes instead
+  const size_t o_xp = c.take(i8 || w8a8 ? 0 : R * d * as);  // int8 weights read the row planes instead
   const size_t o_h = c.take(i8 ? std::max<int64_t>(2 * R, 2 * kDecGateSplitMax * std::min<int64_t>(R, kDecGateSplitRows)) * f * 4
                              : R * f * hs);
   const size_t o_yp = i8 ? c.take(0) : c.take(R * d * hs);
@@ -228,11 +231,13 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   const int64_t part_rows = i8 ? std::max<int64_t>(R, (int64_t)ctx->dec_split * std::min<int64_t>(R, 256)) : 0;
   const size_t o_part = c.take(part_rows * d * 4);
   const size_t plane_w = (size_t)std::max<int64_t>(d, f);
-  const size_t o_phi = c.take(i8 ? R * plane_w : 0), o_plo = c.take(i8 ? R * plane_w : 0);
-  const size_t o_psc = c.take(i8 ? part_rows * 4 : 0);  // per (down K split, row) scales of the H planes
+  // int8 activations: one plane, of the x rows and then of the H rows
+  const size_t o_phi = c.take(i8 || w8a8 ? R * plane_w : 0), o_plo = c.take(i8 ? R * plane_w : 0);
+  const size_t o_psc = c.take(i8 ? part_rows * 4 : (w8a8 ? R * 4 : 0));  // per (down K split, row) scales of the H planes
   const size_t o_err = c.take(4);
   const size_t o_tsched = c.take(4 * 4);
-  const size_t o_flog = c.take(i8 ? 0 : std::min<int64_t>(M, kFewMaxT) * E * 4), o_fbar = c.take(i8 ? 0 : 2 * 4);
+  const bool few = f32 || bf16;  // weight types that colibri_moe_decode takes
+  const size_t o_flog = c.take(few ? std::min<int64_t>(M, kFewMaxT) * E * 4 : 0), o_fbar = c.take(few ? 2 * 4 : 0);
   const size_t o_gbar = c.take(i8 ? kFusedBarCount * 4 : 0);
   ctx->ws_bytes = c.off;
 
@@ -270,10 +275,10 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   w.err = reinterpret_cast<uint32_t*>(b + o_err);
   w.tile_sched = reinterpret_cast<uint32_t*>(b + o_tsched);
   w.few_logits = reinterpret_cast<float*>(b + o_flog);
-  w.few_bar = i8 ? nullptr : reinterpret_cast<int32_t*>(b + o_fbar);
+  w.few_bar = few ? reinterpret_cast<int32_t*>(b + o_fbar) : nullptr;
   w.grid_bar = i8 ? reinterpret_cast<int32_t*>(b + o_gbar) : nullptr;
   if (cudaMemset(w.err, 0, 4) != cudaSuccess || cudaMemset(w.tile_sched, 0, 4 * 4) != cudaSuccess ||
-      (!i8 && cudaMemset(w.few_bar, 0, 2 * 4) != cudaSuccess) ||
+      (few && cudaMemset(w.few_bar, 0, 2 * 4) != cudaSuccess) ||
       (i8 && cudaMemset(w.grid_bar, 0, kFusedBarCount * 4) != cudaSuccess)) {
     cudaFree(ctx->ws_base);
     delete ctx;
@@ -303,6 +308,7 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   if (ce == cudaSuccess) ce = configure_dec_kernels();
   if (ce == cudaSuccess) ce = configure_simt_kernels();
   if (ce == cudaSuccess) ce = configure_few_kernels();
+  if (ce == cudaSuccess && w8a8) ce = configure_int_kernels();
   if (ce != cudaSuccess) {
     cudaGetLastError();
     cudaFree(ctx->ws_base);
@@ -476,18 +482,22 @@ colibri_status enqueue_forward(colibri_ctx* ctx, const void* x, PtrKind xk, int3
   const int bm = D.weight_dtype == COLIBRI_F32 ? kSimtBM : (gemm == kGemmPair ? kTcPairBM : kTcBM);
   const RowPlanes xplanes{w.plane_hi, w.plane_lo, w.plane_scale};
   const RowPlanes* planes = quant ? &xplanes : nullptr;
+  const bool int8_rows = D.weight_dtype == COLIBRI_I8A8;
+  const int copy_d = int8_rows ? 0 : d;  // int8 rows: the scatter only finds the rows, quantising fills them
   if (route_in_dec) {
     // grouping and the x planes are phase 0 of the fused expert launch
   } else if (T <= kFusedRouteMaxT) {
-    COLIBRI_TRY(launch_route_fused(xd, act, T, d, w.topk_idx, k, E, bm, w.counts, w.offsets, w.mt_prefix,
+    COLIBRI_TRY(launch_route_fused(xd, act, T, copy_d, w.topk_idx, k, E, bm, w.counts, w.offsets, w.mt_prefix,
                                    w.src_row, w.dst_row, w.Xp, planes, s), "route_fused");
   } else {
     COLIBRI_TRY(launch_route_count(w.topk_idx, T, k, E, w.blk_counts, w.dst_row, s), "route_count");
     COLIBRI_TRY(launch_route_scan(w.blk_counts, nblk, E, bm, w.blk_base, w.counts, w.offsets, w.mt_prefix, s),
                 "route_scan");
-    COLIBRI_TRY(launch_route_scatter(xd, act, T, d, k, E, w.topk_idx, w.blk_base, w.offsets, w.dst_row, w.src_row,
+    COLIBRI_TRY(launch_route_scatter(xd, act, T, copy_d, k, E, w.topk_idx, w.blk_base, w.offsets, w.dst_row, w.src_row,
                                      w.Xp, planes, s), "route_scatter");
   }
+  if (int8_rows)
+    COLIBRI_TRY(launch_quantize_rows(xd, act, T, d, d, w.plane_hi, d, w.plane_scale, s, w.dst_row, k), "quantize x");
   mark(2);
 
   // ---- Expert compute
@@ -539,6 +549,19 @@ colibri_status enqueue_forward(colibri_ctx* ctx, const void* x, PtrKind xk, int3
     a.A_sh = w.Hs;
     a.out_sh = w.Ys;
     COLIBRI_TRY(launch_tc_down(a, s), "tc_down");
+  } else if (int8_rows) {
+    // gate/up on int8 rows, H rounded to bf16 (as on the other paths) and its rows to int8 in place of
+    // the x rows, down
+    const int8_t* W = (const int8_t*)expert_w;
+    const int64_t scales = 2 * (int64_t)f + d;  // per expert s1 | s3 | s2
+    IntGemmArgs g{w.plane_hi, d, w.plane_scale, R, w.offsets, E, W, stride, d, expert_scales, scales, f, d, w.H, f,
+                  COLIBRI_BF16, w.err};
+    COLIBRI_TRY(launch_int_gemm(g, true, s), "int8 gate/up");
+    mark(3);
+    COLIBRI_TRY(launch_quantize_rows(w.H, COLIBRI_BF16, R, f, f, w.plane_hi, f, w.plane_scale, s), "quantize h");
+    IntGemmArgs dn{w.plane_hi, f, w.plane_scale, R, w.offsets, E, W + 2 * (int64_t)f * d, stride, f,
+                   expert_scales + 2 * (int64_t)f, scales, d, f, w.Yp, d, COLIBRI_BF16, w.err};
+    COLIBRI_TRY(launch_int_gemm(dn, false, s), "int8 down");
   } else {
     // K splits of the down projection: enough work items to cover every SM a few times
     nsplit = 1;
@@ -713,8 +736,8 @@ colibri_status forward_impl(colibri_ctx* ctx, const void* x, int32_t T, const vo
   } else if (!router_w) {
     return fail(ctx, COLIBRI_ERR_INVALID_ARG, "router_w is NULL");
   }
-  const bool quant = D.weight_dtype == COLIBRI_I8 || D.weight_dtype == COLIBRI_I4;
-  if (quant != (expert_scales != nullptr))
+  const bool scaled = D.weight_dtype != COLIBRI_F32 && D.weight_dtype != COLIBRI_BF16;
+  if (scaled != (expert_scales != nullptr))
     return fail(ctx, COLIBRI_ERR_INVALID_ARG, "expert_scales must be given exactly when weights are int8 or int4");
   if ((D.shared_d_ff > 0) != (shared_w != nullptr))
     return fail(ctx, COLIBRI_ERR_INVALID_ARG, "shared_w must be given exactly when shared_d_ff > 0");

@@ -990,6 +990,18 @@ cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s) {
   return swiglu ? launch_pair<true>(a, sms, s) : launch_pair<false>(a, sms, s);
 }
 
+// Loads the kernels a context's forward may launch, so that its first launch may be a captured one.
+cudaError_t configure_int_kernels() {
+  const auto set = [](auto kern, size_t smem) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  };
+  cudaError_t e = set(i8_pair_kernel<true, __nv_bfloat16>, kPairSmem);
+  if (e == cudaSuccess) e = set(i8_pair_kernel<false, __nv_bfloat16>, kPairSmem);
+  if (e == cudaSuccess) e = set(i8_split_kernel<true, __nv_bfloat16>, kSplitSmem);
+  if (e == cudaSuccess) e = set(i8_split_kernel<false, __nv_bfloat16>, kSplitSmem);
+  return e;
+}
+
 // The error word of calls without one of their own, read and cleared (after `s` is idle).
 cudaError_t int_gemm_take_error(uint32_t* word) {
   cudaError_t e = cudaMemcpyFromSymbol(word, g_int_err, sizeof(uint32_t));

@@ -98,7 +98,8 @@ __device__ __forceinline__ uint4 unit_quantize(const Unit16<T>& u, float s, floa
 template <typename T, int TPR, int kQUnits>
 __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 3 : 2) quantize_rows_kernel(const T* __restrict__ x, int rows, int units,
                                                                   int64_t ldx, int8_t* __restrict__ q, int64_t ldq,
-                                                                  float* __restrict__ scale) {
+                                                                  float* __restrict__ scale,
+                                                                  const int32_t* __restrict__ dst, int k) {
   pdl_trigger();
   pdl_wait();
   constexpr int kRows = kQThreads / TPR;
@@ -139,48 +140,63 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 3 : 2) quantize_ro
     }
     if (!finite) s = __uint_as_float(0x7fc00000u);
     if (!live) continue;
-    if (t == 0) scale[r] = s;
     const float inv = 1.f / s;
-    uint4* dst = reinterpret_cast<uint4*>(q + r * ldq);
+    // to row r itself, or to the k rows it is grouped into
+    auto put = [&](int c, const Unit16<T>& v) {
+      const uint4 w = zero ? make_uint4(0, 0, 0, 0) : unit_quantize(v, s, inv);
+      if (!dst) {
+        reinterpret_cast<uint4*>(q + r * ldq)[c] = w;
+        if (c == 0) scale[r] = s;
+        return;
+      }
+#pragma unroll 1
+      for (int j = 0; j < k; ++j) {
+        const int64_t to = dst[r * k + j];
+        reinterpret_cast<uint4*>(q + to * ldq)[c] = w;
+        if (c == 0) scale[to] = s;
+      }
+    };
 #pragma unroll
     for (int i = 0; i < kQUnits; ++i)
-      if (t + i * TPR < units) dst[t + i * TPR] = zero ? make_uint4(0, 0, 0, 0) : unit_quantize(u[i], s, inv);
+      if (t + i * TPR < units) put(t + i * TPR, u[i]);
     for (int c = t + kQUnits * TPR; c < units; c += TPR) {
       Unit16<T> more;
       more.load(src + (size_t)c * 16);
-      dst[c] = zero ? make_uint4(0, 0, 0, 0) : unit_quantize(more, s, inv);
+      put(c, more);
     }
   }
 }
 
 template <typename T, int TPR, int kQUnits>
-cudaError_t launch_q(const T* x, int rows, int units, int64_t ldx, int8_t* q, int64_t ldq, float* scale, cudaStream_t s) {
+cudaError_t launch_q(const T* x, int rows, int units, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
+                     const int32_t* dst, int k, cudaStream_t s) {
   constexpr int kRows = kQThreads / TPR;
   const int grid = std::min((rows + kRows - 1) / kRows, 148 * 64);
   return launch_kernel(quantize_rows_kernel<T, TPR, kQUnits>, dim3(grid), dim3(kQThreads), 0, s, 1, x, rows, units, ldx,
-                       q, ldq, scale);
+                       q, ldq, scale, dst, k);
 }
 
 // The fewest threads per row that hold it in four units each, so that a thread has several loads in
 // flight (4096 x 4096 bf16: 27 us with one unit on each of 256 threads).
 template <typename T>
-cudaError_t launch_q(const T* x, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale, cudaStream_t s) {
+cudaError_t launch_rows(const T* x, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
+                        const int32_t* dst, int k, cudaStream_t s) {
   const int units = cols / 16;
-  if (units <= 32) return launch_q<T, 32, 1>(x, rows, units, ldx, q, ldq, scale, s);
-  if (units <= 64) return launch_q<T, 32, 2>(x, rows, units, ldx, q, ldq, scale, s);
-  if (units <= 128) return launch_q<T, 32, 4>(x, rows, units, ldx, q, ldq, scale, s);
-  if (units <= 256) return launch_q<T, 64, 4>(x, rows, units, ldx, q, ldq, scale, s);
-  if (units <= 512) return launch_q<T, 128, 4>(x, rows, units, ldx, q, ldq, scale, s);
-  return launch_q<T, 256, 4>(x, rows, units, ldx, q, ldq, scale, s);
+  if (units <= 32) return launch_q<T, 32, 1>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
+  if (units <= 64) return launch_q<T, 32, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
+  if (units <= 128) return launch_q<T, 32, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
+  if (units <= 256) return launch_q<T, 64, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
+  if (units <= 512) return launch_q<T, 128, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
+  return launch_q<T, 256, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_rows(const void* x, int act, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,
-                                 float* scale, cudaStream_t s) {
+                                 float* scale, cudaStream_t s, const int32_t* dst, int k) {
   if (rows <= 0) return cudaSuccess;
-  if (act == COLIBRI_BF16) return launch_q((const __nv_bfloat16*)x, rows, cols, ldx, q, ldq, scale, s);
-  return launch_q((const float*)x, rows, cols, ldx, q, ldq, scale, s);
+  if (act == COLIBRI_BF16) return launch_rows((const __nv_bfloat16*)x, rows, cols, ldx, q, ldq, scale, dst, k, s);
+  return launch_rows((const float*)x, rows, cols, ldx, q, ldq, scale, dst, k, s);
 }
 
 }  // namespace colibri
