@@ -237,7 +237,10 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   const size_t o_err = c.take(4);
   const size_t o_tsched = c.take(4 * 4);
   const bool few = f32 || bf16;  // weight types that colibri_moe_decode takes
-  const size_t o_flog = c.take(few ? std::min<int64_t>(M, kFewMaxT) * E * 4 : 0), o_fbar = c.take(few ? 2 * 4 : 0);
+  const size_t o_flog = c.take(few ? std::min<int64_t>(M, kFewMaxT) * E * 4 : 0), o_fbar = c.take(few ? kFewBarCount * 4 : 0);
+  const int64_t fewM = std::min<int64_t>(M, kFewMaxT);
+  const size_t o_fhlo = c.take(bf16 ? fewM * D.top_k * f * 2 : 0), o_fhslo = c.take(bf16 ? fewM * fs * 2 : 0);
+  const size_t o_fpart = c.take(few ? few_part_floats((int)fewM, ctx->sm_count) * 4 : 0);
   const size_t o_gbar = c.take(i8 ? kFusedBarCount * 4 : 0);
   ctx->ws_bytes = c.off;
 
@@ -275,10 +278,13 @@ colibri_status colibri_init(const colibri_desc* desc, colibri_ctx** out) {
   w.err = reinterpret_cast<uint32_t*>(b + o_err);
   w.tile_sched = reinterpret_cast<uint32_t*>(b + o_tsched);
   w.few_logits = reinterpret_cast<float*>(b + o_flog);
+  w.few_hlo = b + o_fhlo;
+  w.few_hslo = b + o_fhslo;
+  w.few_part = reinterpret_cast<float*>(b + o_fpart);
   w.few_bar = few ? reinterpret_cast<int32_t*>(b + o_fbar) : nullptr;
   w.grid_bar = i8 ? reinterpret_cast<int32_t*>(b + o_gbar) : nullptr;
   if (cudaMemset(w.err, 0, 4) != cudaSuccess || cudaMemset(w.tile_sched, 0, 4 * 4) != cudaSuccess ||
-      (few && cudaMemset(w.few_bar, 0, 2 * 4) != cudaSuccess) ||
+      (few && cudaMemset(w.few_bar, 0, kFewBarCount * 4) != cudaSuccess) ||
       (i8 && cudaMemset(w.grid_bar, 0, kFusedBarCount * 4) != cudaSuccess)) {
     cudaFree(ctx->ws_base);
     delete ctx;
@@ -432,6 +438,9 @@ colibri_status enqueue_forward(colibri_ctx* ctx, const void* x, PtrKind xk, int3
     fa.W_sh = shared_w;
     fa.H = w.H;
     fa.Hs = w.Hs;
+    fa.Hlo = w.few_hlo;
+    fa.Hslo = w.few_hslo;
+    fa.part = w.few_part;
     fa.y = yd;
     fa.logits = w.few_logits;
     fa.topk_idx = w.topk_idx;
@@ -960,7 +969,7 @@ colibri_status colibri_sync_status(colibri_ctx* ctx, void* stream) {
     // a wait that gave up may leave the fused kernel's grid-barrier counters out of step
     if (ctx->ws.grid_bar)
       COLIBRI_TRY(cudaMemset(ctx->ws.grid_bar, 0, kFusedBarCount * 4), "reset grid-barrier counters");
-    if (ctx->ws.few_bar) COLIBRI_TRY(cudaMemset(ctx->ws.few_bar, 0, 2 * 4), "reset grid-barrier counters");
+    if (ctx->ws.few_bar) COLIBRI_TRY(cudaMemset(ctx->ws.few_bar, 0, kFewBarCount * 4), "reset grid-barrier counters");
     COLIBRI_TRY(cudaMemset(ctx->ws.tile_sched, 0, 4 * 4), "reset tile counters");
     return fail(ctx, COLIBRI_ERR_TIMEOUT, "device error word 0x%x (a bounded wait gave up)", err);
   }

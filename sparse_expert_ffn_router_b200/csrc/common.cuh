@@ -82,7 +82,10 @@ struct Workspace {
   float* plane_scale = nullptr;  // [M*k]
   uint32_t* err = nullptr;
   float* few_logits = nullptr;   // [min(M, kFewMaxT), E] few-token path
-  int32_t* few_bar = nullptr;    // [2] its grid-barrier counters (zero at first use)
+  void* few_hlo = nullptr;       // bf16: [min(M, kFewMaxT)*k, f], second part of its H
+  void* few_hslo = nullptr;      // bf16: [min(M, kFewMaxT), fs]
+  float* few_part = nullptr;     // partial sums of its split down projection
+  int32_t* few_bar = nullptr;    // [3] its grid-barrier counters (zero at first use)
   uint32_t* tile_sched = nullptr;  // [4] tile counters of the bf16 GEMMs (gate/up, down; zero between calls)
 };
 
@@ -361,6 +364,10 @@ cudaError_t launch_dec_fused(const DecFusedArgs& a, cudaStream_t s);
 
 // ---- the whole layer for a few tokens in one launch (few_tokens.cu)
 constexpr int kFewMaxT = 16;
+constexpr int kFewBarCount = 3;
+constexpr int kFewRowsW = 32;            // weight rows of a tile: 4 per lane
+// a split down projection has at most one part of 32 columns per CTA
+inline size_t few_part_floats(int T, int sm_count) { return (size_t)T * kFewRowsW * sm_count; }
 struct FewArgs {
   const void* x;           // [T, d] act
   const void* router_w;    // [E, d] act
@@ -370,12 +377,15 @@ struct FewArgs {
   const void* W_sh;        // shared expert or nullptr (fs == 0)
   void* H;                 // [T*k, f] act
   void* Hs;                // [T, fs] act
+  void* Hlo;               // bf16: [T*k, f] and [T, fs], the second parts of H and Hs
+  void* Hslo;
+  float* part;             // [few_part_floats(T, sm_count)]
   void* y;                 // [T, d] act
   float* logits;           // [T, E]
   int32_t* topk_idx;       // routing state as every forward leaves it
   float* topk_w;
   int32_t *counts, *offsets, *src_row, *dst_row;
-  int32_t* bar;            // [2] grid-barrier counters: zero at first use, then owned by the kernel
+  int32_t* bar;            // [kFewBarCount] grid-barrier counters: zero at first use, then owned by the kernel
   uint32_t* err;
   int T, d, f, fs, E, k, router_flags, sm_count;
 };

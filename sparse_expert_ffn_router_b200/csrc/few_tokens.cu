@@ -14,7 +14,9 @@
 //            expert they fall in.
 //   down     every CTA owns an equal share of the output columns, for all touched experts, so the
 //            weighted sum is formed where it is needed, in ascending expert order: no third
-//            barrier, no atomics, the same bits in every run.
+//            barrier, no atomics, the same bits in every run.  Where that would leave a CTA fewer
+//            than kFewSplitRows columns (a lane's loads would mostly have no row), 32 columns go to
+//            a team of CTAs that split the sum, and a third barrier lets all CTAs add the parts up.
 // The shares are split to single columns (a partly filled last tile loads only its own rows), so
 // that no CTA reads more than one row above the average.
 //
@@ -28,8 +30,10 @@
 // projections.  bf16: mma.m16n8k16, weights as the 16-row operand (8 gate rows and the 8 up rows of
 // the same columns; for down 16 output columns), tokens as the 8 columns; the order of k inside an
 // instruction is free, so a lane's 16 bytes of a weight row feed two instructions as they are, and
-// the token operand is 16 bytes of the token's row.  fp32: FMA on the CUDA cores.  H is kept in the
-// activation type between the projections (bf16: rounded once), as on the library's other paths.
+// the token operand is 16 bytes of the token's row.  fp32: FMA on the CUDA cores.  H is kept as fp32, or
+// as two bf16 (its rounding and what that left, 2^-17 in all): one rounding to bf16 would double the
+// variance of the output's own rounding error, and the second product costs nothing that the weight
+// stream would notice.
 #include "common.cuh"
 
 namespace colibri {
@@ -38,10 +42,10 @@ namespace {
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kFewDepth = 4;             // ring stages of a warp
-constexpr int kFewRowsW = 32;            // weight rows of a tile: 4 per lane
 constexpr int kFewStage = 4 * 512;       // bytes of a warp's stage: 4 rows of 16 bytes per lane
 constexpr int kFewEntries = kFewMaxT * kMaxTopK + 1;  // touched experts and the shared one
 constexpr int kFewPitch = kFewMaxT + 2;  // floats per weight row of the partial sums (16 token columns)
+constexpr int kFewSplitRows = 9;         // fewer output columns per CTA: the down projection is split
 constexpr int kFewBatch = 16;            // gate/up tiles whose partial sums meet at a time
 constexpr int kFewSlot = kFewRowsW * kFewPitch;       // floats of one warp's partial sums of one tile
 
@@ -81,11 +85,14 @@ struct FewParams {
   const T* Ws;         // shared expert or nullptr
   T* H;                // [T*k, f]
   T* Hs;               // [T, fs]
+  T* Hlo;              // bf16: what rounding left of H and Hs, as bf16 again
+  T* Hslo;
+  float* part;         // [splits, T, d] partial sums of a split down projection
   T* y;                // [T, d]
   float* logits;       // [T, E]
   int32_t *topk_idx, *counts, *offsets, *src_row, *dst_row;
   float* topk_w;
-  int32_t* bar;        // [2]
+  int32_t* bar;        // [3]
   uint32_t* err;
   int T_, d, f, fs, E, k, flags;
   int tg;              // router: tokens per task
@@ -103,7 +110,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 // The runs of chunks of one CTA.  Gate/up: the gate columns of all entries laid end to end, cut into
 // tiles of 16 (every width is a multiple of 64, so a tile lies in one entry); the CTA owns columns
 // [c0, c1) and takes their tiles in batches.  Down: the CTA owns output columns [o0, o1), in groups of
-// 32, each group over the chunks of all entries laid end to end.
+// 32, each group over the chunks [d0, d1) of all entries laid end to end.
 template <typename T>
 struct FewShare {
   static constexpr int CE = 64 / sizeof(T);  // elements of a chunk
@@ -111,33 +118,48 @@ struct FewShare {
   int o0, o1;
   int tiles, batches, groups;
   int cd, cf, cs;  // chunks of a row of d, f, fs elements
-  int down_chunks;
+  int d0, d1;      // down: this CTA's run over the chunks of all entries
+  int teams, splits, split;  // down, split: teams of `splits` CTAs, and this CTA's place in its team (teams 0: not)
   int fs, f;
 
   __device__ FewShare(const FewParams<T>& p, int n_ent) {
     fs = p.fs;
     f = p.f;
     const int routed = n_ent - (fs > 0 ? 1 : 0);
-    split(fs + routed * f, c0, c1);  // at most 129 * 2^18 columns
-    split(p.d, o0, o1);
+    const int G = gridDim.x, b = blockIdx.x;
+    cut(fs + routed * f, G, b, c0, c1);  // at most 129 * 2^18 columns
     tiles = c1 > c0 ? (c1 + 15) / 16 - c0 / 16 : 0;
     batches = (tiles + kFewBatch - 1) / kFewBatch;
-    groups = (o1 - o0 + kFewRowsW - 1) / kFewRowsW;
     cd = p.d / CE;
     cf = f / CE;
     cs = fs / CE;
-    down_chunks = cs + routed * cf;
+    d0 = 0;
+    d1 = cs + routed * cf;
+    teams = 0;
+    if (p.d < kFewSplitRows * G) {
+      teams = (p.d + kFewRowsW - 1) / kFewRowsW;
+      splits = G / teams;
+      const int team = b % teams;
+      split = b / teams;
+      groups = split < splits ? 1 : 0;
+      o0 = team * kFewRowsW;
+      o1 = min(p.d, o0 + kFewRowsW);
+      if (groups) cut(d1, splits, split, d0, d1);
+    } else {
+      cut(p.d, G, b, o0, o1);
+      groups = (o1 - o0 + kFewRowsW - 1) / kFewRowsW;
+    }
   }
-  // this CTA's part of n columns: equal to one column
-  __device__ static __forceinline__ void split(int n, int& a, int& b) {
-    const int G = gridDim.x, i = blockIdx.x, each = n / G, rest = n - each * G;
+  // part i of n things in G nearly equal parts
+  __device__ static __forceinline__ void cut(int n, int G, int i, int& a, int& b) {
+    const int each = n / G, rest = n - each * G;
     a = each * i + min(i, rest);
     b = a + each + (i < rest ? 1 : 0);
   }
   __device__ __forceinline__ int batch_tiles(int s) const { return min(kFewBatch, tiles - s * kFewBatch); }
   // chunks that warp w takes of the batch or group
   __device__ __forceinline__ int begin(int phase, int s, int w) const {
-    return (phase == 0 ? batch_tiles(s) * cd : down_chunks) * w / kFewWarps;
+    return phase == 0 ? batch_tiles(s) * cd * w / kFewWarps : d0 + (d1 - d0) * w / kFewWarps;
   }
 };
 
@@ -300,10 +322,12 @@ struct FewAcc<float, NT> {
 
 // `n` chunks of the stream times the columns' rows.  Column j of `cols` has its row at row(j) elements
 // behind `rows` (row(j) < 0: the column is zero); `at`: the first chunk's element.  kH: the rows were
-// written by this launch (read them from L2); scale(j) multiplies the column's values (fp32 only).
+// written by this launch (read them from L2; bf16: their second part lies `lo` elements behind the
+// first); scale(j) multiplies the column's values (fp32 only).
 template <typename T, int NT, bool kH, typename Row, typename Scale>
-__device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int& slot, int n, const T* rows, int at,
-                                           Row row, Scale scale, FewAcc<T, NT>& acc, int lane) {
+__device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int& slot, int n, const T* rows, int64_t lo,
+                                           int at, Row row, Scale scale, FewAcc<T, NT>& acc, int lane) {
+  constexpr int P = kH && sizeof(T) == 2 ? 2 : 1;
   const int g = lane >> 2, t = lane & 3;
   constexpr int CE = 64 / sizeof(T);
   auto load = [](const T* s) {
@@ -319,19 +343,23 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
   }
   // a lane holds 16 bytes of the columns g and g + 8; those of the next chunk are loaded while this
   // one is multiplied
-  uint4 xn[NT];
+  uint4 xn[P][NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    xn[j] = make_uint4(0, 0, 0, 0);
-    if (src[j]) xn[j] = load(src[j]);
-  }
-  for (int i = 0; i < n; ++i) {
-    uint4 xb[NT];
+  for (int h = 0; h < P; ++h)
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      xb[j] = xn[j];
-      if (src[j] && i + 1 < n) xn[j] = load(src[j] + (i + 1) * CE);
+      xn[h][j] = make_uint4(0, 0, 0, 0);
+      if (src[j]) xn[h][j] = load(src[j] + h * lo);
     }
+  for (int i = 0; i < n; ++i) {
+    uint4 xb[P][NT];
+#pragma unroll
+    for (int h = 0; h < P; ++h)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        xb[h][j] = xn[h][j];
+        if (src[j] && i + 1 < n) xn[h][j] = load(src[j] + h * lo + (i + 1) * CE);
+      }
     cp_async_wait<kFewDepth - 1>();
     uint4 wq[4];
     const uint32_t from = ring + slot * kFewStage;
@@ -340,28 +368,33 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
     slot = slot + 1 == kFewDepth ? 0 : slot + 1;
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int h = 0; h < P; ++h)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma_bf16(acc.v[m][j], wq[2 * m].x, wq[2 * m + 1].x, wq[2 * m].y, wq[2 * m + 1].y, xb[j].x, xb[j].y);
-          mma_bf16(acc.v[m][j], wq[2 * m].z, wq[2 * m + 1].z, wq[2 * m].w, wq[2 * m + 1].w, xb[j].z, xb[j].w);
-        }
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint4& x = xb[h][j];
+            mma_bf16(acc.v[m][j], wq[2 * m].x, wq[2 * m + 1].x, wq[2 * m].y, wq[2 * m + 1].y, x.x, x.y);
+            mma_bf16(acc.v[m][j], wq[2 * m].z, wq[2 * m + 1].z, wq[2 * m].w, wq[2 * m + 1].w, x.z, x.w);
+          }
     } else {
       // every lane needs every column's bytes: they come from the lane that loaded them
 #pragma unroll
       for (int j = 0; j < 8 * NT; ++j) {
         if (row(j) < 0) continue;
-        const uint4& x = xb[j >> 3];
+        const uint4& x = xb[0][j >> 3];
         const float s = sc[j >> 3];
         float xs[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
 #pragma unroll
         for (int k = 0; k < 4; ++k) xs[k] = __shfl_sync(0xffffffffu, kH ? xs[k] * s : xs[k], (j & 7) * 4 + t);
+        // four products first, then one addition to the long sum: a quarter of its roundings
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          acc.v[q][j] = fmaf(xs[0], __uint_as_float(wq[q].x), acc.v[q][j]);
-          acc.v[q][j] = fmaf(xs[1], __uint_as_float(wq[q].y), acc.v[q][j]);
-          acc.v[q][j] = fmaf(xs[2], __uint_as_float(wq[q].z), acc.v[q][j]);
-          acc.v[q][j] = fmaf(xs[3], __uint_as_float(wq[q].w), acc.v[q][j]);
+          float four = xs[0] * __uint_as_float(wq[q].x);
+          four = fmaf(xs[1], __uint_as_float(wq[q].y), four);
+          four = fmaf(xs[2], __uint_as_float(wq[q].z), four);
+          four = fmaf(xs[3], __uint_as_float(wq[q].w), four);
+          acc.v[q][j] += four;
         }
       }
     }
@@ -376,7 +409,7 @@ __device__ __forceinline__ void few_gate_up(FewStream<T>& st, uint32_t ring, int
   FewAcc<T, NT> acc;
   acc.clear();
   few_chunks<T, NT, false>(
-      st, ring, slot, sg.left, x, sg.chunk * (64 / (int)sizeof(T)),
+      st, ring, slot, sg.left, x, 0, sg.chunk * (64 / (int)sizeof(T)),
       [&](int j) { return j < ntok ? (int64_t)tok[j] * d : (int64_t)-1; }, [](int) { return 1.f; }, acc, lane);
   acc.store(red, lane);
 }
@@ -394,6 +427,7 @@ __device__ __forceinline__ void few_down(FewStream<T>& st, uint32_t ring, int& s
     const bool shared = c.ent_e[sg.ent] < 0;
     const int f = shared ? p.fs : p.f;
     const T* H = (shared ? p.Hs : p.H) + (int64_t)c.ent_row[sg.ent] * f;
+    const int64_t lo = sizeof(T) == 2 ? (shared ? p.Hslo - p.Hs : p.Hlo - p.H) : 0;
     const uint32_t mask = c.ent_mask[sg.ent];
     const float* wt = c.ent_w[sg.ent];
     auto row = [&](int j) { return mask >> j & 1u ? (int64_t)__popc(mask & ((1u << j) - 1u)) * f : (int64_t)-1; };
@@ -402,7 +436,7 @@ __device__ __forceinline__ void few_down(FewStream<T>& st, uint32_t ring, int& s
     if constexpr (sizeof(T) == 2) {
       FewAcc<T, NT> acc;
       acc.clear();
-      few_chunks<T, NT, true>(st, ring, slot, sg.left, H, at, row, scale, acc, lane);
+      few_chunks<T, NT, true>(st, ring, slot, sg.left, H, lo, at, row, scale, acc, lane);
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -418,7 +452,7 @@ __device__ __forceinline__ void few_down(FewStream<T>& st, uint32_t ring, int& s
           }
         }
     } else {
-      few_chunks<T, NT, true>(st, ring, slot, sg.left, H, at, row, scale, sum, lane);
+      few_chunks<T, NT, true>(st, ring, slot, sg.left, H, lo, at, row, scale, sum, lane);
     }
     pos += sg.left;
   }
@@ -609,6 +643,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_tokens_kernel(const __grid
   few_router(p, c);
   if (!few_barrier(p, c, 0)) {
     few_barrier(p, c, 1);
+    if (p.d < kFewSplitRows * (int)gridDim.x) few_barrier(p, c, 2);
     return;
   }
   few_select(p, c, red);
@@ -649,8 +684,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_tokens_kernel(const __grid
       }
       const bool shared = c.ent_e[sg.ent] < 0;
       const int f = shared ? p.fs : p.f;
-      T* H = (shared ? p.Hs : p.H) + (int64_t)(c.ent_row[sg.ent] + n) * f;
-      H[sg.col + col] = from_f32<T>(silu_mul(gt, up));
+      const int64_t at = (int64_t)(c.ent_row[sg.ent] + n) * f + sg.col + col;
+      const float v = silu_mul(gt, up);
+      const T hi = from_f32<T>(v);
+      (shared ? p.Hs : p.H)[at] = hi;
+      if (sizeof(T) == 2) (shared ? p.Hslo : p.Hlo)[at] = from_f32<T>(v - to_f32(hi));
     }
     __syncthreads();
   }
@@ -666,11 +704,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_tokens_kernel(const __grid
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) v += red[w * kFewSlot + lane * kFewPitch + warp];
-      p.y[(int64_t)warp * p.d + o] = from_f32<T>(v);
+      if (h.teams) p.part[((int64_t)h.split * p.T_ + warp) * p.d + o] = v;
+      else p.y[(int64_t)warp * p.d + o] = from_f32<T>(v);
     }
     __syncthreads();
   }
   cp_async_wait<0>();
+  if (h.teams && few_barrier(p, c, 2)) {
+    const int n = p.T_ * p.d;
+    for (int i = blockIdx.x * kFewThreads + threadIdx.x; i < n; i += gridDim.x * kFewThreads) {
+      float v = 0.f;
+#pragma unroll 8
+      for (int s = 0; s < h.splits; ++s) v += __ldcg(p.part + (int64_t)s * n + i);
+      p.y[i] = from_f32<T>(v);
+    }
+  }
 }
 
 template <typename T>
@@ -684,6 +732,9 @@ cudaError_t launch_few(const FewArgs& a, cudaStream_t s) {
   p.Ws = (const T*)a.W_sh;
   p.H = (T*)a.H;
   p.Hs = (T*)a.Hs;
+  p.Hlo = (T*)a.Hlo;
+  p.Hslo = (T*)a.Hslo;
+  p.part = a.part;
   p.y = (T*)a.y;
   p.logits = a.logits;
   p.topk_idx = a.topk_idx;

@@ -4,10 +4,12 @@ The tolerance of every output value is a bound formed beside the reference, with
 step r of the activation type (2^-8 for bf16, u for fp32, where H and y are fp32 anyway):
 
 * a dot product of n terms is off by at most n u times the sum of the terms' magnitudes, in any order
-  (bf16 products are exact in fp32; an fp32 multiply-add rounds once), plus one addition per partial sum,
-  at most 32 of them: (n + 32) u in all;
+  (bf16 products are exact in fp32; an fp32 product rounds once), plus one addition per partial sum.
+  Sums are cut into runs of 16 or 32 terms and more, so besides the runs' own additions there are at most
+  n / 16 of them that are not zero, which the runs leave room for, and 32 where warps meet: (n + 32) u;
 * h = silu(g) * v: |silu'| <= 1.1, and the exponential, quotient and product are good to (24 + 8 |g|) u;
-  then one rounding to the activation type, r |h|;
+  h is kept as fp32, or as two bf16: what the first leaves is at most r |h|, and of that the second
+  leaves r again, r^2 |h| = 2^-16 |h| in all;
 * the weight of a chosen expert: its logit and the largest are each off by at most el, which enters the
   softmax with at most 4 el, and exponential, sum and quotient add less than 32 u (raw weights: el);
 * the weighted sum over k experts and the shared one adds (k + 2) u of the magnitudes, and y is rounded
@@ -22,6 +24,7 @@ F32, BF16 = colibri.COLIBRI_F32, colibri.COLIBRI_BF16
 TORCH = {F32: torch.float32, BF16: torch.bfloat16}
 U = 2.0 ** -24
 HALF = {F32: U, BF16: torch.finfo(torch.bfloat16).eps / 2}
+HALF_H = {F32: U, BF16: HALF[BF16] ** 2}
 
 
 def test_decode_refuses_a_null_context():
@@ -58,7 +61,7 @@ class Case:
     def _ffn(self, w, width, x):
         """FFN of rows x in 64 bits and the bound on its error."""
         w = w.double()
-        d, half = self.d, HALF[self.dt]
+        d, half = self.d, HALF_H[self.dt]
         w1, w3, w2 = w[: width * d].view(width, d), w[width * d: 2 * width * d].view(width, d), w[2 * width * d: 3 * width * d].view(d, width)
         g, v, xa = x @ w1.T, x @ w3.T, x.abs()
         eg, ev = (d + 32) * U * (xa @ w1.abs().T), (d + 32) * U * (xa @ w3.abs().T)
@@ -129,7 +132,8 @@ class Case:
     (1, 64, 64, 1, 1, 0), (1, 64, 64, 1, 1, 64), (2, 64, 128, 3, 3, 0), (3, 256, 512, 8, 2, 0), (16, 128, 64, 2, 1, 192),
     (1, 2048, 768, 128, 4, 1536), (7, 192, 320, 256, 8, 64), (8, 1024, 704, 16, 8, 0), (9, 576, 1088, 2, 2, 128),
     (15, 320, 2048, 5, 5, 0), (16, 64, 64, 256, 8, 0), (16, 4096, 192, 6, 2, 0), (5, 8192, 64, 3, 2, 64), (12, 4992, 128, 4, 1, 0),
-    (4, 64, 14336, 2, 2, 0), (1, 4096, 1536, 8, 2, 0), (16, 512, 512, 1, 1, 512), (6, 16384, 64, 2, 1, 0),
+    (4, 64, 14336, 2, 2, 0), (1, 4096, 1536, 8, 2, 0), (2, 192, 6208, 20, 8, 320), (16, 1280, 448, 30, 5, 64),
+    (3, 1344, 320, 9, 3, 0), (16, 1152, 64, 3, 1, 0), (16, 512, 512, 1, 1, 512), (6, 16384, 64, 2, 1, 0),
 ])
 def test_decode(T, d, f, E, k, fs, dt):
     c = Case(T, d, f, E, k, fs, dt, bias=E > 4)
