@@ -133,7 +133,7 @@ class Case:
     (1, 2048, 768, 128, 4, 1536), (7, 192, 320, 256, 8, 64), (8, 1024, 704, 16, 8, 0), (9, 576, 1088, 2, 2, 128),
     (15, 320, 2048, 5, 5, 0), (16, 64, 64, 256, 8, 0), (16, 4096, 192, 6, 2, 0), (5, 8192, 64, 3, 2, 64), (12, 4992, 128, 4, 1, 0),
     (4, 64, 14336, 2, 2, 0), (1, 4096, 1536, 8, 2, 0), (2, 192, 6208, 20, 8, 320), (16, 1280, 448, 30, 5, 64),
-    (3, 1344, 320, 9, 3, 0), (16, 1152, 64, 3, 1, 0), (16, 512, 512, 1, 1, 512), (6, 16384, 64, 2, 1, 0),
+    (3, 1344, 320, 9, 3, 0), (16, 1152, 64, 3, 1, 0), (10, 2048, 192, 40, 3, 64), (2, 2368, 832, 7, 2, 0), (16, 2432, 64, 4, 2, 0), (16, 512, 512, 1, 1, 512), (6, 16384, 64, 2, 1, 0),
 ])
 def test_decode(T, d, f, E, k, fs, dt):
     c = Case(T, d, f, E, k, fs, dt, bias=E > 4)
