@@ -61,6 +61,8 @@ struct FewCtl {
   uint32_t ent_mask[kFewEntries];
   uint8_t ent_tok[kFewEntries][kFewMaxT];
   float ent_w[kFewEntries][kFewMaxT];    // weight by token
+  int32_t warp_rows[kMaxExperts / 32];   // while selecting
+  int32_t warp_has[kMaxExperts / 32];
   int32_t n_ent;
   int32_t ok;
   int32_t abort;
@@ -330,8 +332,14 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
   constexpr int P = kH && sizeof(T) == 2 ? 2 : 1;
   const int g = lane >> 2, t = lane & 3;
   constexpr int CE = 64 / sizeof(T);
+  // volatile: the compiler would move the loads for the next chunk behind the wait for this one
   auto load = [](const T* s) {
-    return kH ? __ldcg(reinterpret_cast<const uint4*>(s)) : __ldg(reinterpret_cast<const uint4*>(s));
+    uint4 v;
+    if (kH)
+      asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(s) : "memory");
+    else
+      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(s) : "memory");
+    return v;
   };
   const T* src[NT];
   float sc[NT];
@@ -459,33 +467,38 @@ __device__ __forceinline__ void few_down(FewStream<T>& st, uint32_t ring, int& s
   sum.store(red, lane);
 }
 
-// Logits: one task per (expert, tg tokens); a CTA's threads split d.
+// Logits: one task per (expert, tg tokens); a CTA's threads split d, B token rows at a time.
+template <typename T, int B>
+__device__ __forceinline__ void few_logits(const FewParams<T>& p, FewCtl& c, const uint4* wr, int t0, int nt, int tb) {
+  const int nvec = p.d / (16 / (int)sizeof(T)), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint4* xr = reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + tb) * p.d);
+  float acc[B];
+#pragma unroll
+  for (int i = 0; i < B; ++i) acc[i] = 0.f;
+  for (int v = threadIdx.x; v < nvec; v += kFewThreads) {
+    const uint4 w = __ldg(wr + v);
+    uint4 x[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) x[i] = __ldg(xr + (int64_t)(tb + i < nt ? i : 0) * nvec + v);
+#pragma unroll
+    for (int i = 0; i < B; ++i) acc[i] = dot16(x[i], w, acc[i], p.x);
+  }
+#pragma unroll
+  for (int i = 0; i < B; ++i) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (lane == 0 && tb + i < nt) c.part[warp][tb + i] = acc[i];
+  }
+}
 template <typename T>
 __device__ __forceinline__ void few_router(const FewParams<T>& p, FewCtl& c) {
-  constexpr int V = 16 / sizeof(T);
-  constexpr int B = 4;  // token rows whose loads are in flight together
-  const int nvec = p.d / V, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntg = (p.T_ + p.tg - 1) / p.tg;
   for (int task = blockIdx.x; task < p.E * ntg; task += gridDim.x) {
     const int e = task / ntg, t0 = (task - e * ntg) * p.tg, nt = min(p.tg, p.T_ - t0);
     const uint4* wr = reinterpret_cast<const uint4*>(p.router_w + (int64_t)e * p.d);
-    for (int tb = 0; tb < nt; tb += B) {
-      const uint4* xr = reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + tb) * p.d);
-      float acc[B] = {0.f, 0.f, 0.f, 0.f};
-      for (int v = threadIdx.x; v < nvec; v += kFewThreads) {
-        const uint4 w = __ldg(wr + v);
-        uint4 x[B];
-#pragma unroll
-        for (int i = 0; i < B; ++i) x[i] = __ldg(xr + (int64_t)(tb + i < nt ? i : 0) * nvec + v);
-#pragma unroll
-        for (int i = 0; i < B; ++i) acc[i] = dot16(x[i], w, acc[i], p.x);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < B; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-      if (lane < B && tb + lane < nt) c.part[warp][tb + lane] = lane == 0 ? acc[0] : lane == 1 ? acc[1] : lane == 2 ? acc[2] : acc[3];
-    }
+    if (nt <= 2) few_logits<T, 2>(p, c, wr, t0, nt, 0);
+    else
+      for (int tb = 0; tb < nt; tb += 8) few_logits<T, 8>(p, c, wr, t0, nt, tb);
     __syncthreads();
     if (threadIdx.x < nt) {
       float s = 0.f;
@@ -497,30 +510,38 @@ __device__ __forceinline__ void few_router(const FewParams<T>& p, FewCtl& c) {
   }
 }
 
-// One warp selects the top-k of one token from its E logits in shared memory (which it overwrites):
-// the largest value first, lower index on ties.  The values are compared as integers in their order
-// (adding zero makes -0 and 0 the same value), so that a step is two warp reductions.
-__device__ __forceinline__ void few_topk(float* lg, int E, int k, int flags, int lane, int32_t* idx, float* w) {
-  uint32_t* key = reinterpret_cast<uint32_t*>(lg);
-  for (int e = lane; e < E; e += 32) {
-    const uint32_t b = __float_as_uint(router_clamp(lg[e], flags) + 0.f);
-    key[e] = max(1u, b & 0x80000000u ? ~b : b | 0x80000000u);  // 0: chosen already
+// One warp selects the top-k of one token from its E logits in shared memory: the largest value first,
+// lower index on ties.  The values are compared as integers in their order (adding zero makes -0 and 0
+// the same value), so that a step is two warp reductions; the experts chosen are distinct whatever the
+// values are.
+__device__ __forceinline__ void few_topk(const float* lg, int E, int k, int flags, int lane, int32_t* idx, float* w) {
+  uint32_t key[kMaxExperts / 32];
+#pragma unroll
+  for (int m = 0; m < kMaxExperts / 32; ++m) {
+    const int e = lane + 32 * m;
+    key[m] = 0u;  // no such expert, or chosen already
+    if (e < E) {
+      const uint32_t b = __float_as_uint(router_clamp(lg[e], flags) + 0.f);
+      key[m] = max(1u, b & 0x80000000u ? ~b : b | 0x80000000u);
+    }
   }
   float den = 0.f, first = 0.f, mine = 0.f;
   int at = 0;
 #pragma unroll 1
   for (int j = 0; j < k; ++j) {
-    uint32_t best = 0;
-    int e_best = 0;
-#pragma unroll 1
-    for (int e = lane; e < E; e += 32)
-      if (key[e] > best) {
-        best = key[e];
-        e_best = e;
+    uint32_t best = key[0];
+    int e_best = lane;
+#pragma unroll
+    for (int m = 1; m < kMaxExperts / 32; ++m)
+      if (key[m] > best) {
+        best = key[m];
+        e_best = lane + 32 * m;
       }
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
     const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)e_best : 0xffffffffu);
-    if ((e & 31) == lane) key[e] = 0u;
+#pragma unroll
+    for (int m = 0; m < kMaxExperts / 32; ++m)
+      if (e == lane + 32 * m) key[m] = 0u;
     const float v = __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
     if (j == 0) first = v;
     const float p = (flags & kRouterRaw) ? v : expf(v - first);
@@ -542,70 +563,75 @@ template <typename T>
 __device__ __forceinline__ void few_select(const FewParams<T>& p, FewCtl& c, float* lg) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = p.k, E = p.E, T_ = p.T_;
   for (int i = threadIdx.x; i < T_ * E; i += kFewThreads) lg[i] = __ldcg(p.logits + i);
-  for (int e = threadIdx.x; e < E; e += kFewThreads) c.mask[e] = 0;
+  if (threadIdx.x < kMaxExperts) c.mask[threadIdx.x] = 0;
   __syncthreads();
   if (warp < T_) {
     few_topk(lg + warp * E, E, k, p.flags, lane, c.idx + warp * k, c.w + warp * k);
     __syncwarp();
-    if (lane < k) {
-      const int e = min(max(c.idx[warp * k + lane], 0), E - 1);
-      c.idx[warp * k + lane] = e;
-      atomicOr(&c.mask[e], 1u << warp);
-    }
+    if (lane < k) atomicOr(&c.mask[c.idx[warp * k + lane]], 1u << warp);
   }
   __syncthreads();
-  if (warp == 0) {
-    int n = p.fs > 0 ? 1 : 0, row = 0;
-    if (n && lane == 0) {
+  // warp w: experts 32 w + lane; rows and touched experts before them by the warps' totals
+  const int e = threadIdx.x, shared = p.fs > 0 ? 1 : 0;
+  uint32_t m = 0, has = 0;
+  int cnt = 0, incl = 0;
+  if (warp < kMaxExperts / 32) {
+    m = c.mask[e];
+    cnt = incl = __popc(m);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += a;
+    }
+    has = __ballot_sync(0xffffffffu, cnt > 0);
+    if (lane == 31) {
+      c.warp_rows[warp] = incl;
+      c.warp_has[warp] = __popc(has);
+    }
+  } else if (warp == kMaxExperts / 32 && shared) {
+    if (lane == 0) {
       c.ent_e[0] = -1;
       c.ent_row[0] = 0;
       c.ent_n[0] = T_;
       c.ent_mask[0] = (1u << T_) - 1u;
     }
-    if (n && lane < kFewMaxT) {
+    if (lane < kFewMaxT) {
       c.ent_tok[0][lane] = (uint8_t)lane;
       c.ent_w[0][lane] = 1.f;
     }
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      const uint32_t m = e < E ? c.mask[e] : 0u;
-      const int cnt = __popc(m);
-      int incl = cnt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += a;
-      }
-      const uint32_t has = __ballot_sync(0xffffffffu, cnt > 0);
-      if (e < E) c.off[e] = row + incl - cnt;
-      if (cnt > 0) {
-        const int i = n + __popc(has & ((1u << lane) - 1u));
-        c.ent_e[i] = e;
-        c.ent_row[i] = row + incl - cnt;
-        c.ent_n[i] = cnt;
-        c.ent_mask[i] = m;
-        c.mask[e] = m | (uint32_t)i << 16;  // the entry beside the tokens
-        uint32_t left = m;
-        for (int j = 0; left; ++j, left &= left - 1) c.ent_tok[i][j] = (uint8_t)(__ffs(left) - 1);
-      }
-      n += __popc(has);
-      row += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __syncthreads();
+  if (warp < kMaxExperts / 32) {
+    int row = 0, n = shared;
+    for (int w = 0; w < warp; ++w) {
+      row += c.warp_rows[w];
+      n += c.warp_has[w];
     }
-    if (lane == 0) {
-      c.n_ent = n;
-      c.off[E] = row;
+    if (e <= E) c.off[e] = row + incl - cnt;
+    if (e == kMaxExperts - 1) c.off[kMaxExperts] = row + incl;
+    if (lane == 31 && warp == kMaxExperts / 32 - 1) c.n_ent = n + __popc(has);
+    if (cnt > 0) {
+      const int i = n + __popc(has & ((1u << lane) - 1u));
+      c.ent_e[i] = e;
+      c.ent_row[i] = row + incl - cnt;
+      c.ent_n[i] = cnt;
+      c.ent_mask[i] = m;
+      c.mask[e] = m | (uint32_t)i << 16;  // the entry beside the tokens
+      uint32_t left = m;
+      for (int j = 0; left; ++j, left &= left - 1) c.ent_tok[i][j] = (uint8_t)(__ffs(left) - 1);
     }
   }
   __syncthreads();
   if (threadIdx.x < T_ * k) c.ent_w[c.mask[c.idx[threadIdx.x]] >> 16][threadIdx.x / k] = c.w[threadIdx.x];
+  __syncthreads();
   if (blockIdx.x == 0) {
-    for (int e = threadIdx.x; e <= E; e += kFewThreads) {
-      p.offsets[e] = c.off[e];
-      if (e < E) p.counts[e] = __popc(c.mask[e] & 0xffffu);
+    for (int i = threadIdx.x; i <= E; i += kFewThreads) {
+      p.offsets[i] = c.off[i];
+      if (i < E) p.counts[i] = __popc(c.mask[i] & 0xffffu);
     }
     for (int i = threadIdx.x; i < T_ * k; i += kFewThreads) {
-      const int t = i / k, e = c.idx[i], r = c.off[e] + __popc(c.mask[e] & ((1u << t) - 1u));
-      p.topk_idx[i] = e;
+      const int t = i / k, ex = c.idx[i], r = c.off[ex] + __popc(c.mask[ex] & ((1u << t) - 1u));
+      p.topk_idx[i] = ex;
       p.topk_w[i] = c.w[i];
       p.dst_row[i] = r;
       p.src_row[r] = t;
@@ -647,7 +673,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_tokens_kernel(const __grid
     return;
   }
   few_select(p, c, red);
-  __syncthreads();
 
   const FewShare<T> h(p, c.n_ent);
   const uint32_t ring = smem_u32(smem) + warp * (kFewDepth * kFewStage) + lane * 16;
