@@ -23,8 +23,7 @@
 // Inside a CTA the 16 warps split the inner dimension: all tiles' chunks of 64 bytes of a row, laid
 // end to end, go to the warps in equal runs, so a warp crosses tiles and experts without meeting the
 // others.  Partial sums meet in shared memory, in warp order, once per 16 tiles (gate/up) or once per
-// 32 output columns (down: a warp adds its experts up in registers, the columns of its partial sums
-// being the tokens).  Each lane keeps its weights in flight through a ring of shared memory that the
+// 32 output columns (down: a warp adds its experts up, weighted, in its own part of it).  Each lane keeps its weights in flight through a ring of shared memory that the
 // same lane fills (cp.async) and drains: no lane reads what another lane copied, so the ring needs
 // no barrier, and a warp's copies run ahead across tiles, experts and the barrier between the two
 // projections.  bf16: mma.m16n8k16, weights as the 16-row operand (8 gate rows and the 8 up rows of
@@ -58,7 +57,6 @@ struct FewCtl {
   int32_t ent_e[kFewEntries];            // expert, or -1: shared
   int32_t ent_row[kFewEntries];          // first row in H (shared: Hs)
   int32_t ent_n[kFewEntries];            // tokens
-  uint32_t ent_mask[kFewEntries];
   uint8_t ent_tok[kFewEntries][kFewMaxT];
   float ent_w[kFewEntries][kFewMaxT];    // weight by token
   int32_t warp_rows[kMaxExperts / 32];   // while selecting
@@ -299,6 +297,25 @@ struct FewAcc<__nv_bfloat16, NT> {
           *reinterpret_cast<float2*>(red + ((2 * m + i) * 8 + g) * kFewPitch + 8 * j + 2 * t) =
               make_float2(v[m][j][2 * i], v[m][j][2 * i + 1]);
   }
+  // the sums of column j, times its weight, onto column tok[j] of red
+  __device__ __forceinline__ void add(float* red, const uint8_t* tok, const float* w, int n, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int col = 8 * j + 2 * t + b;
+        if (col < n) {
+          const int to = tok[col];
+          const float wt = w[to];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float* d = red + (q * 8 + g) * kFewPitch + to;
+            *d = fmaf(wt, v[q >> 1][j][2 * (q & 1) + b], *d);
+          }
+        }
+      }
+  }
 };
 template <int NT>
 struct FewAcc<float, NT> {
@@ -320,15 +337,31 @@ struct FewAcc<float, NT> {
         if ((j & 3) == t) red[(q * 8 + g) * kFewPitch + j] = v[q][j];
       }
   }
+  __device__ __forceinline__ void add(float* red, const uint8_t* tok, const float* w, int n, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 8 * NT; ++j)
+      if (j < n) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float x = v[q][j];
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          if ((j & 3) == t) {
+            float* d = red + (q * 8 + g) * kFewPitch + tok[j];
+            *d = fmaf(w[tok[j]], x, *d);
+          }
+        }
+      }
+  }
 };
 
-// `n` chunks of the stream times the columns' rows.  Column j of `cols` has its row at row(j) elements
-// behind `rows` (row(j) < 0: the column is zero); `at`: the first chunk's element.  kH: the rows were
-// written by this launch (read them from L2; bf16: their second part lies `lo` elements behind the
-// first); scale(j) multiplies the column's values (fp32 only).
-template <typename T, int NT, bool kH, typename Row, typename Scale>
+// `n` chunks of the stream times the rows of `ncol` columns; column j has its row at row(j) elements
+// behind `rows`; `at`: the first chunk's element.  kH: the rows were written by this launch (read them
+// from L2; bf16: their second part lies `lo` elements behind the first).
+template <typename T, int NT, bool kH, typename Row>
 __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int& slot, int n, const T* rows, int64_t lo,
-                                           int at, Row row, Scale scale, FewAcc<T, NT>& acc, int lane) {
+                                           int at, int ncol, Row row, FewAcc<T, NT>& acc, int lane) {
   constexpr int P = kH && sizeof(T) == 2 ? 2 : 1;
   const int g = lane >> 2, t = lane & 3;
   constexpr int CE = 64 / sizeof(T);
@@ -342,31 +375,32 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
     return v;
   };
   const T* src[NT];
-  float sc[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t r = row(g + 8 * j);
-    src[j] = r < 0 ? nullptr : rows + r + at + t * (16 / (int)sizeof(T));
-    sc[j] = kH && r >= 0 ? scale(g + 8 * j) : 1.f;
-  }
-  // a lane holds 16 bytes of the columns g and g + 8; those of the next chunk are loaded while this
-  // one is multiplied
-  uint4 xn[P][NT];
+  for (int j = 0; j < NT; ++j)
+    src[j] = g + 8 * j < ncol ? rows + row(g + 8 * j) + at + t * (16 / (int)sizeof(T)) : nullptr;
+  // a lane holds 16 bytes of the columns g and g + 8; those of the next chunk are loaded while this one is
+  // multiplied; the parts of H, which come from L2, two chunks ahead (16 tokens 465 -> 457 us; for x,
+  // mostly in L1, a second measured slower, and two blocks of columns have no registers for it)
+  constexpr int D = kH && NT == 1 ? 2 : 1;
+  uint4 xn[D][P][NT];
 #pragma unroll
-  for (int h = 0; h < P; ++h)
+  for (int k = 0; k < D; ++k)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      xn[h][j] = make_uint4(0, 0, 0, 0);
-      if (src[j]) xn[h][j] = load(src[j] + h * lo);
-    }
+    for (int h = 0; h < P; ++h)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        xn[k][h][j] = make_uint4(0, 0, 0, 0);
+        if (src[j] && k < n) xn[k][h][j] = load(src[j] + h * lo + k * CE);
+      }
   for (int i = 0; i < n; ++i) {
     uint4 xb[P][NT];
 #pragma unroll
     for (int h = 0; h < P; ++h)
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        xb[h][j] = xn[h][j];
-        if (src[j] && i + 1 < n) xn[h][j] = load(src[j] + h * lo + (i + 1) * CE);
+        xb[h][j] = xn[0][h][j];
+        if (D == 2) xn[0][h][j] = xn[D - 1][h][j];
+        if (src[j] && i + D < n) xn[D - 1][h][j] = load(src[j] + h * lo + (i + D) * CE);
       }
     cp_async_wait<kFewDepth - 1>();
     uint4 wq[4];
@@ -389,12 +423,11 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
       // every lane needs every column's bytes: they come from the lane that loaded them
 #pragma unroll
       for (int j = 0; j < 8 * NT; ++j) {
-        if (row(j) < 0) continue;
+        if (j >= ncol) continue;
         const uint4& x = xb[0][j >> 3];
-        const float s = sc[j >> 3];
         float xs[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) xs[k] = __shfl_sync(0xffffffffu, kH ? xs[k] * s : xs[k], (j & 7) * 4 + t);
+        for (int k = 0; k < 4; ++k) xs[k] = __shfl_sync(0xffffffffu, xs[k], (j & 7) * 4 + t);
         // four products first, then one addition to the long sum: a quarter of its roundings
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -416,55 +449,41 @@ __device__ __forceinline__ void few_gate_up(FewStream<T>& st, uint32_t ring, int
                                             int d, const uint8_t* tok, int ntok, float* red, int lane) {
   FewAcc<T, NT> acc;
   acc.clear();
-  few_chunks<T, NT, false>(
-      st, ring, slot, sg.left, x, 0, sg.chunk * (64 / (int)sizeof(T)),
-      [&](int j) { return j < ntok ? (int64_t)tok[j] * d : (int64_t)-1; }, [](int) { return 1.f; }, acc, lane);
+  few_chunks<T, NT, false>(st, ring, slot, sg.left, x, 0, sg.chunk * (64 / (int)sizeof(T)), ntok,
+                           [&](int j) { return (int64_t)tok[j] * d; }, acc, lane);
   acc.store(red, lane);
 }
 
 // Down of one group of 32 output columns: this warp's run over all entries, partial sums
-// [32 columns][tokens] of the weighted sum into red.
+// [32 columns][tokens] of the weighted sum into red (each value is one lane's alone).
 template <typename T, int NT>
+__device__ __forceinline__ void few_down_segment(FewStream<T>& st, uint32_t ring, int& slot, const FewSeg& sg, const T* H,
+                                                 int64_t lo, int f, const uint8_t* tok, const float* w, int ntok,
+                                                 float* red, int lane) {
+  FewAcc<T, NT> acc;
+  acc.clear();
+  few_chunks<T, NT, true>(st, ring, slot, sg.left, H, lo, sg.chunk * (64 / (int)sizeof(T)), ntok,
+                          [&](int j) { return (int64_t)j * f; }, acc, lane);
+  acc.add(red, tok, w, ntok, lane);
+}
+template <typename T>
 __device__ __forceinline__ void few_down(FewStream<T>& st, uint32_t ring, int& slot, const FewParams<T>& p,
                                          const FewCtl& c, const FewShare<T>& h, int s, int warp, float* red, int lane) {
-  FewAcc<T, NT> sum;
-  sum.clear();
+  for (int i = lane; i < kFewSlot; i += 32) red[i] = 0.f;
+  __syncwarp();
   const int end = h.begin(1, s, warp + 1);
   for (int pos = h.begin(1, s, warp); pos < end;) {
     const FewSeg sg = few_segment(h, 1, s, pos, end);
     const bool shared = c.ent_e[sg.ent] < 0;
-    const int f = shared ? p.fs : p.f;
+    const int f = shared ? p.fs : p.f, ntok = c.ent_n[sg.ent];
     const T* H = (shared ? p.Hs : p.H) + (int64_t)c.ent_row[sg.ent] * f;
     const int64_t lo = sizeof(T) == 2 ? (shared ? p.Hslo - p.Hs : p.Hlo - p.H) : 0;
-    const uint32_t mask = c.ent_mask[sg.ent];
-    const float* wt = c.ent_w[sg.ent];
-    auto row = [&](int j) { return mask >> j & 1u ? (int64_t)__popc(mask & ((1u << j) - 1u)) * f : (int64_t)-1; };
-    auto scale = [&](int j) { return wt[j]; };
-    const int at = sg.chunk * (64 / (int)sizeof(T));
-    if constexpr (sizeof(T) == 2) {
-      FewAcc<T, NT> acc;
-      acc.clear();
-      few_chunks<T, NT, true>(st, ring, slot, sg.left, H, lo, at, row, scale, acc, lane);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int col = 8 * j + 2 * (lane & 3) + b;
-          if (mask >> col & 1u) {
-            const float w = wt[col];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              sum.v[m][j][b] = fmaf(w, acc.v[m][j][b], sum.v[m][j][b]);
-              sum.v[m][j][2 + b] = fmaf(w, acc.v[m][j][2 + b], sum.v[m][j][2 + b]);
-            }
-          }
-        }
-    } else {
-      few_chunks<T, NT, true>(st, ring, slot, sg.left, H, lo, at, row, scale, sum, lane);
-    }
+    const uint8_t* tok = c.ent_tok[sg.ent];
+    const float* w = c.ent_w[sg.ent];
+    if (ntok <= 8) few_down_segment<T, 1>(st, ring, slot, sg, H, lo, f, tok, w, ntok, red, lane);
+    else few_down_segment<T, 2>(st, ring, slot, sg, H, lo, f, tok, w, ntok, red, lane);
     pos += sg.left;
   }
-  sum.store(red, lane);
 }
 
 // Logits: one task per (expert, tg tokens); a CTA's threads split d, B token rows at a time.
@@ -593,7 +612,6 @@ __device__ __forceinline__ void few_select(const FewParams<T>& p, FewCtl& c, flo
       c.ent_e[0] = -1;
       c.ent_row[0] = 0;
       c.ent_n[0] = T_;
-      c.ent_mask[0] = (1u << T_) - 1u;
     }
     if (lane < kFewMaxT) {
       c.ent_tok[0][lane] = (uint8_t)lane;
@@ -615,7 +633,6 @@ __device__ __forceinline__ void few_select(const FewParams<T>& p, FewCtl& c, flo
       c.ent_e[i] = e;
       c.ent_row[i] = row + incl - cnt;
       c.ent_n[i] = cnt;
-      c.ent_mask[i] = m;
       c.mask[e] = m | (uint32_t)i << 16;  // the entry beside the tokens
       uint32_t left = m;
       for (int j = 0; left; ++j, left &= left - 1) c.ent_tok[i][j] = (uint8_t)(__ffs(left) - 1);
@@ -721,8 +738,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_tokens_kernel(const __grid
   // H of every CTA is written; the copies of the first W2 chunks are already in flight
   const bool ok = few_barrier(p, c, 1);
   for (int s = 0; ok && s < h.groups; ++s) {
-    if (p.T_ <= 8) few_down<T, 1>(st, ring, slot, p, c, h, s, warp, red + warp * kFewSlot, lane);
-    else few_down<T, 2>(st, ring, slot, p, c, h, s, warp, red + warp * kFewSlot, lane);
+    few_down(st, ring, slot, p, c, h, s, warp, red + warp * kFewSlot, lane);
     __syncthreads();
     const int o = h.o0 + s * kFewRowsW + lane;
     if (warp < p.T_ && o < h.o1) {
