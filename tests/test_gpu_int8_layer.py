@@ -143,3 +143,27 @@ def test_layer_stage_events():
         layer.forward(t["x"], t["router_w"], None, t["expert_w"], y, t["expert_scales"], stream=st)
     ms, n = colibri.colibri_profile_end(layer.ctx)
     assert n == 4 and all(v > 0 for v in ms.values())
+
+
+@pytest.mark.gpu
+def test_layer_overlapped_launches(monkeypatch):
+    # programmatic dependent launch only starts a kernel's set-up early: the same bits, as plain launches
+    # and as a replayed graph
+    wl = _wl(260, 256, 6, 2, 448)
+    p = inputgen.make_problem(wl, seed=5)
+    t = H.to_device(p)
+    outs = []
+    for pdl in ("0", "1"):
+        monkeypatch.setenv("COLIBRI_PDL", pdl)
+        layer = _layer(wl)
+        s = torch.cuda.Stream()
+        for stream in (None, s, s):
+            y = torch.full((wl.T, wl.d), 5.0, dtype=torch.bfloat16, device="cuda")
+            torch.cuda.synchronize()
+            layer.forward(t["x"], t["router_w"], None, t["expert_w"], y, t["expert_scales"], stream=stream)
+            torch.cuda.synchronize()
+            outs.append(y)
+        layer.sync_status()
+        layer.close()
+    for y in outs[1:]:
+        assert torch.equal(y, outs[0])
