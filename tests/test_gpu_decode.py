@@ -300,3 +300,34 @@ def test_decode_stage_events_count_the_launch():
     ms, n = colibri.colibri_profile_end(c.layer.ctx)
     assert n == 4 and ms["expert_gateup"] > 0
     assert ms["expert_gateup"] > sum(v for k, v in ms.items() if k != "expert_gateup")
+
+
+@pytest.mark.gpu
+def test_decode_experts_past_32_bits():
+    # the last experts start more than 2^31 elements into the weight buffer
+    c = Case(2, 4096, 14336, 14, 2)
+    assert 13 * c.layer.expert_stride > 1 << 31
+    c.rb = torch.zeros(14, device="cuda")
+    c.rb[12:] = 30.0
+    c.check(c.decode())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_decode_weights_that_are_not_finite_stay_with_their_tokens(dt):
+    # an expert whose weights are broken touches only the tokens that chose it
+    c = Case(6, 128, 192, 4, 1, 0, dt)
+    c.x.zero_()
+    c.x[:3, 0], c.x[3:, 1] = 1.0, 1.0
+    c.x[:, 2:] = 0.25
+    c.rw.zero_()
+    c.rw[1, 0], c.rw[2, 1] = 9.0, 9.0            # tokens 0-2 take expert 1, tokens 3-5 expert 2
+    clean = c.decode().clone()
+    f, d = c.f, c.d
+    c.ew[2, 5] = float("inf")
+    c.ew[2, 2 * f * d: 3 * f * d] = float("nan")
+    c.ew[0] = c.ew[3] = float("nan")             # experts that nobody takes
+    y = c.decode()
+    torch.cuda.synchronize()
+    assert c.routing()["topk_idx"].flatten().tolist() == [1, 1, 1, 2, 2, 2]
+    assert torch.equal(y[:3], clean[:3]) and torch.isnan(y[3:]).all()

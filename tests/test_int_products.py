@@ -469,3 +469,85 @@ def test_expert_ffn_from_the_parts(T, d, f, E, act):
     terms = wt.cpu().double()[:, :, None] * yp.cpu().double()[dst.cpu().long()]
     bound = terms.abs().sum(1) * 2 * k * U + terms.sum(1).abs() * HALF[act] * 1.001
     assert ((y.cpu().double() - terms.sum(1)).abs() <= bound + 1e-37).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("counts", [(1, 2), (150, 40)])
+def test_offsets_past_32_bits(counts, swiglu):
+    """Rows, experts and output rows that lie more than 2^31 bytes (and elements) apart."""
+    c = _experts_case(counts, 48, 64, 3, swiglu)
+    R, N, K, cols = c["R"], 48, 64, c["w"].shape[1]
+    far = (1 << 31) // (R - 1) // 16 * 16 + 16       # the last row starts past 2^31 elements
+    w_stride = (1 << 31) + 16
+    a = torch.empty(far * (R - 1) + K, dtype=torch.int8, device="cuda")
+    rows = torch.arange(R, device="cuda")[:, None] * far
+    a[rows + torch.arange(K, device="cuda")] = c["q"].cuda()
+    w = torch.empty(w_stride + cols * K, dtype=torch.int8, device="cuda")
+    for e in range(2):
+        w[e * w_stride: e * w_stride + cols * K] = c["w"][e].reshape(-1).cuda()
+    y = torch.empty(far * (R - 1) + N, dtype=torch.bfloat16, device="cuda")
+    s, t, off = c["s"].cuda(), c["t"].cuda(), c["off"].cuda()
+    call = colibri.colibri_int_swiglu_experts if swiglu else colibri.colibri_int_gemm_experts
+    call(a, far, s, R, off, 2, w, w_stride, t, cols, N, K, y, far, BF16, torch.cuda.current_stream())
+    colibri.colibri_int_check(torch.cuda.current_stream())
+    _check_experts(c, y[rows + torch.arange(N, device="cuda")].cpu(), BF16)
+    if not swiglu:
+        q, sq, wt = c["q"], c["s"], c["w"][1]
+        y.zero_()
+        colibri.colibri_int_gemm(a, far, s, w.data_ptr() + w_stride, K, t[1], R, N, K, y, far, BF16,
+                                 torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        _check(y[rows + torch.arange(N, device="cuda")].cpu(), _ref_product(q, sq, wt, c["t"][1]), 4 * U, BF16)
+    xq, xs = torch.empty(far * (R - 1) + K, dtype=torch.int8, device="cuda"), torch.empty(R, device="cuda")
+    x = torch.empty(far * (R - 1) + K, dtype=torch.bfloat16, device="cuda")
+    xv = torch.randn(R, K, device="cuda").bfloat16()
+    x[rows + torch.arange(K, device="cuda")] = xv
+    colibri.colibri_quantize_rows(x, BF16, R, K, far, xq, far, xs)
+    torch.cuda.synchronize()
+    rq, rs = _ref_quantize(xv.cpu())
+    assert torch.equal(xq[rows + torch.arange(K, device="cuda")].cpu(), rq) and torch.equal(xs.cpu(), rs)
+
+
+@pytest.mark.gpu
+def test_check_reports_nothing_after_good_calls():
+    q, s, w, t = _problem(300, 300, 256, 8)
+    _run_gemm(q, s, w, t, F32)
+    colibri.colibri_int_check()
+    colibri.colibri_int_check(torch.cuda.Stream())
+
+
+@pytest.mark.gpu
+def test_two_host_threads():
+    """Context-free calls from two host threads, each with its own stream and its own last error."""
+    import threading
+
+    probs = [_problem(90, 700, 512, 21), _problem(9, 333, 1024, 22)]
+    alone = [_run_gemm(*p, F32) for p in probs]
+    dev = [[v.cuda() for v in p] for p in probs]
+    torch.cuda.synchronize()
+    out, errors = [None, None], []
+
+    def work(i):
+        try:
+            q, s, w, t = dev[i]
+            st = torch.cuda.Stream()
+            y = torch.empty(q.shape[0], w.shape[0], device="cuda")
+            st.wait_stream(torch.cuda.default_stream())
+            for _ in range(50):
+                colibri.colibri_int_gemm(q, q.shape[1], s, w, q.shape[1], t, q.shape[0], w.shape[0], q.shape[1], y, w.shape[0], F32, st)
+                _refused(INVALID, _gemm, K=8 + 16 * i, lda=64)
+                assert f"K={8 + 16 * i}" in colibri.colibri_last_error()
+            st.synchronize()
+            out[i] = y.cpu()
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors, errors
+    for y, ref in zip(out, alone):
+        assert torch.equal(y, ref)
