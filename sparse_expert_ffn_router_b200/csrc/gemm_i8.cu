@@ -263,8 +263,50 @@ __device__ __forceinline__ void tmem_ld_wait16(int (&v)[16]) {
                : "memory");
 }
 
-// silu(g) * u; the quotient by the approximate division (2 ulp)
-__device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// Two fp32 values per instruction: the epilogue is bound by the instructions it issues.
+struct Pair {
+  unsigned long long v;
+};
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ void halves(const Pair& p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ Pair operator*(const Pair& a, const Pair& b) {
+  Pair p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+__device__ __forceinline__ Pair operator+(const Pair& a, const Pair& b) {
+  Pair p;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// silu(g) * u = g / (1 + 2^(-g log2 e)) * u.  The exponential is good to 2^-22 and the rounding of its
+// argument, the reciprocal to 2^-23; what they flush (an exponential below 2^-126, a reciprocal of one
+// above 2^126) does not show beside the 1, or is below 1e-36.
+__device__ __forceinline__ Pair silu_mul(const Pair& g, const Pair& u) {
+  float a, b;
+  halves(g * pair_of(-1.44269504f, -1.44269504f), a, b);
+  halves(pair_of(exp2_approx(a), exp2_approx(b)) + pair_of(1.f, 1.f), a, b);
+  return g * pair_of(rcp_approx(a), rcp_approx(b)) * u;
+}
+__device__ __forceinline__ float silu_mul_fast(float g, float u) {
+  return g * rcp_approx(1.f + exp2_approx(g * -1.44269504f)) * u;
+}
 
 // 16 values of this lane's row into the gathered block, at byte `at` of its 128.
 template <typename Out>
@@ -590,17 +632,17 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
         };
         auto finish = [&](int c, const int (&g)[16], const int (&u)[16]) {
           float v[16];
+          const Pair s2 = pair_of(sr, sr);
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            const float4 tg = *reinterpret_cast<const float4*>(col + c + i);
-            const float tgs[4] = {tg.x, tg.y, tg.z, tg.w};
+            const ulonglong2 tg = *reinterpret_cast<const ulonglong2*>(col + c + i);
+            const ulonglong2 tu = *reinterpret_cast<const ulonglong2*>(col + (kSwiglu ? kBN / 2 : 0) + c + i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[i + j] = (float)g[i + j] * (sr * tgs[j]);
-            if (kSwiglu) {
-              const float4 tu = *reinterpret_cast<const float4*>(col + kBN / 2 + c + i);
-              const float tus[4] = {tu.x, tu.y, tu.z, tu.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[i + j] = silu_mul_fast(v[i + j], (float)u[i + j] * (sr * tus[j]));
+            for (int j = 0; j < 4; j += 2) {
+              Pair r = pair_of((float)g[i + j], (float)g[i + j + 1]) * (s2 * Pair{j ? tg.y : tg.x});
+              if (kSwiglu)
+                r = silu_mul(r, pair_of((float)u[i + j], (float)u[i + j + 1]) * (s2 * Pair{j ? tu.y : tu.x}));
+              halves(r, v[i + j], v[i + j + 1]);
             }
           }
           gather16<Out>(block, lane, c * (int)sizeof(Out) & (kOutRow - 1), v);
