@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
         const Tile t = m.tile[slot];
         mbar_arrive(&m.pfree[slot]);
         const int a = it & 1;
-        if (!wait_or_abort<true>(&m.tempty[a], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag)) {
+        if (!wait_or_abort(&m.tempty[a], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
         const uint32_t idesc = light ? idesc_s8_s32(kBM, (trows + 31) / 32 * 32) : idesc_s8_s32(kBM, kBN);
         const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
         for (int step = 0; step < steps; ++step) {
-          if (!wait_or_abort<true>(&m.full[s], ph, abort_flag)) {
+          if (!wait_or_abort(&m.full[s], ph, abort_flag)) {
             ok = false;
             break;
           }
