@@ -1,7 +1,7 @@
 // The whole MoE layer for at most 16 tokens in one cooperative launch (bf16 or fp32 weights, with
 // the shared expert): router, top-k, gate/up, down, weighted sum.
 //
-//   logits[t][e] = x_t . Wr_e + b_e;  the k chosen experts and their weights p (warp_topk)
+//   logits[t][e] = x_t . Wr_e + b_e;  the k chosen experts and their weights p (few_topk)
 //   h[t][e]      = silu(W1_e x_t) * (W3_e x_t)
 //   y[t]         = sum_(e chosen by t) p[t][e] W2_e h[t][e]  (+ W2_s h_s[t])
 //
@@ -17,22 +17,30 @@
 //            barrier, no atomics, the same bits in every run.  Where that would leave a CTA fewer
 //            than kFewSplitRows columns (a lane's loads would mostly have no row), 32 columns go to
 //            a team of CTAs that split the sum, and a third barrier lets all CTAs add the parts up.
-// The shares are split to single columns (a partly filled last tile loads only its own rows), so
-// that no CTA reads more than one row above the average.
+// The shares are split to single columns (a partly filled tile loads only its own rows), so that no
+// CTA reads more than one row above the average.
 //
 // Inside a CTA the 16 warps split the inner dimension: all tiles' chunks of 64 bytes of a row, laid
 // end to end, go to the warps in equal runs, so a warp crosses tiles and experts without meeting the
 // others.  Partial sums meet in shared memory, in warp order, once per 16 tiles (gate/up) or once per
-// 32 output columns (down: a warp adds its experts up, weighted, in its own part of it).  Each lane keeps its weights in flight through a ring of shared memory that the
-// same lane fills (cp.async) and drains: no lane reads what another lane copied, so the ring needs
-// no barrier, and a warp's copies run ahead across tiles, experts and the barrier between the two
-// projections.  bf16: mma.m16n8k16, weights as the 16-row operand (8 gate rows and the 8 up rows of
-// the same columns; for down 16 output columns), tokens as the 8 columns; the order of k inside an
-// instruction is free, so a lane's 16 bytes of a weight row feed two instructions as they are, and
-// the token operand is 16 bytes of the token's row.  fp32: FMA on the CUDA cores.  H is kept as fp32, or
-// as two bf16 (its rounding and what that left, 2^-17 in all): one rounding to bf16 would double the
-// variance of the output's own rounding error, and the second product costs nothing that the weight
-// stream would notice.
+// 32 output columns (down: a warp adds its experts up, weighted, in its own part of it); meeting after
+// every tile cost 2 us per tile.  Each lane keeps its weights in flight through a ring of shared memory
+// that the same lane fills (cp.async) and drains: no lane reads what another lane copied, so the ring
+// needs no barrier, and a warp's copies run ahead across tiles, experts and the barrier between the
+// two projections.  The copies fetch 256 bytes of a row at a time into L2 (a warp walks along rows 64
+// bytes per step; without that one token took 141 us instead of 124).  bf16: mma.m16n8k16, weights as
+// the 16-row operand (8 gate rows and the 8 up rows of the same columns; for down 16 output columns),
+// tokens as the 8 columns; the order of k inside an instruction is free, so a lane's 16 bytes of a weight
+// row feed two instructions as they are, and the token operand is 16 bytes of the token's row.  fp32:
+// FMA on the CUDA cores.  H is kept as fp32, or as two bf16 (its rounding and what that left, 2^-16 in
+// all): one rounding to bf16 would double the variance of the output's own rounding error (0.0023
+// against 0.0017 of the output's norm); the second product costs 4 us of 70 on 128 small experts and
+// nothing measurable on large ones.
+//
+// Measured (B200, copy bandwidth 6455 GB/s): d = 4096, f = 14336, 8 experts, top-2, bf16: 1 token (704 MB)
+// 120 us, 5.9 TB/s; 16 tokens (2.8 GB) 461 us, 6.1 TB/s.  128 experts of d = 2048, f = 768, top-4, with a
+// shared expert of 1536: 8 tokens (291 MB) 69 us.  A layer of 256 x 512: 18.5 us, latency alone
+// (logits 2.5, selection 1.8, gate/up 5, down 2, the barriers 2 each, the launch 3).
 #include "common.cuh"
 
 namespace colibri {

@@ -26,12 +26,21 @@
 // share weight tiles through L2; groups of a single m-tile (streams of weights) are interleaved with
 // the others in proportion.  Pair i takes tiles i, i + pairs, ...
 //
+// What bounds a full tile: a stage of 64 KB per pair feeds 512 cycles of MMAs (8192 multiply-adds per
+// cycle and SM) and takes 0.37-0.44 us, against 0.28 us for the MMAs alone at 1.81 GHz: the MMAs read 64
+// bytes of shared memory per cycle and SM while the copies write 64, which is all that one SM's shared
+// memory has.  Measured (B200): 4096 x 14336 x 4096 164 us = 2.9 POP/s, the tensor pipe busy 69 % of the time,
+// 1.9 GB from L2; rows of 8 experts times [2 x 14336, 4096] with SwiGLU 694 us = 2.8 POP/s (830 us when
+// it runs without a pause under the power cap); 64 rows on 8 experts (940 MB of weights) 148 us = 6.4 TB/s.
+// With little k per tile the epilogue bounds it (1.9 us per 256 x 256 tile).
+//
 // i8_split_kernel: products of too few pair tiles to occupy the GPU.  Tiles of 128 x 128 (one CTA each,
 // cta_group::1) whose k range is split over the S = 1, 2 or 4 CTAs of a cluster; the int32 partial
 // sums, exact in any order, are exchanged through the cluster's shared memory (the idle ring), each
 // CTA finishing 1 / S of the columns.  What bounds such a product is the feed of one SM's shared
 // memory (about 100 GB/s measured, against 43 GB/s of HBM per SM), so the SMs left idle are worth more
-// than the larger tile: 4096 x 4096 at 128 rows 19.4 us as pair tiles.
+// than the larger tile: 4096 x 4096 at 128 rows 12.5 us against 19.4 as pair tiles, 4096 x 14336 at 64 rows
+// 18.6 against 43; 14336 x 4096 at 256 rows has 224 such tiles and stays with the pairs (21 us).
 //
 // Every wait is bounded (kWaitTimeoutNs); one that gives up sets the error word and ends all roles.
 #include <algorithm>
@@ -1025,7 +1034,7 @@ cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // Fewer tiles of 128 x 128 than SMs: one CTA per tile, or with k split 2 or 4 CTAs, all at once;
-  // more tiles keep the pair kernel's SMs busy.
+  // more tiles keep the pair kernel's SMs busy (both sides: the header comment).
   const int groups = a.offsets ? a.E : 1, cols = swiglu ? kSplitTile / 2 : kSplitTile;
   const long long tiles = (a.offsets ? (long long)a.rows / kSplitTile + groups : (a.rows + kSplitTile - 1) / kSplitTile) *
                           ((a.N + cols - 1) / cols);

@@ -17,7 +17,9 @@
 //
 // Bound by memory: a row is read once, kept in registers while its maximum is formed, and written
 // once (3 bytes per bf16 element).  Each thread owns units of 16 elements (two or four 16-byte
-// loads, one 16-byte store).  4096 x 4096 bf16: 21 us with the comparison made for every value.
+// loads, one 16-byte store).  Measured (B200): 16384 x 16384 bf16 142 us = 5.7 TB/s, fp32 195 us = 6.9 TB/s;
+// 4096 x 4096 bf16 16.5 us = 3.1 TB/s, two waves of latency (21 us with the comparison made for every
+// value).
 #include <algorithm>
 
 #include "common.cuh"
