@@ -8,7 +8,7 @@
 // With a few tokens every touched expert's weights are read once and meet a few rows, so the work
 // is a stream over those weights (2 or 4 bytes per 2 x tokens FLOP) and the bound is HBM.  Three
 // phases, two grid barriers between them:
-//   router   CTA e (round-robin) forms the logits of expert e for all tokens.
+//   router   the logits, one task per expert and a few tokens, the tasks over the CTAs.
 //   gate/up  every CTA selects the experts of all tokens from the logits (the same result in each),
 //            then owns an equal share of the gate columns of all touched experts together, whatever
 //            expert they fall in.
@@ -738,7 +738,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_tokens_kernel(const __grid
       const float v = silu_mul(gt, up);
       const T hi = from_f32<T>(v);
       (shared ? p.Hs : p.H)[at] = hi;
-      if (sizeof(T) == 2) (shared ? p.Hslo : p.Hlo)[at] = from_f32<T>(v - to_f32(hi));
+      if (sizeof(T) == 2)  // nothing is left of an infinity
+        (shared ? p.Hslo : p.Hlo)[at] = from_f32<T>(fabsf(to_f32(hi)) < INFINITY ? v - to_f32(hi) : 0.f);
     }
     __syncthreads();
   }

@@ -331,3 +331,20 @@ def test_decode_weights_that_are_not_finite_stay_with_their_tokens(dt):
     torch.cuda.synchronize()
     assert c.routing()["topk_idx"].flatten().tolist() == [1, 1, 1, 2, 2, 2]
     assert torch.equal(y[:3], clean[:3]) and torch.isnan(y[3:]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_decode_infinite_activations_stay_infinite(dt):
+    # h overflows in one expert: its products are infinities of their weights' signs, as h alone would give
+    c = Case(2, 64, 64, 2, 1, 0, dt)
+    c.x.fill_(1.0)
+    c.rw.zero_()
+    c.ew.zero_()
+    f, d = c.f, c.d
+    w = c.ew[0]
+    w[0:d], w[f * d: f * d + d] = 2.0 ** 60, 2.0 ** 62       # g = 2^66, u = 2^68: h[0] = 2^134 overflows
+    w[2 * f * d: 3 * f * d].view(d, f)[:, 0] = torch.where(torch.arange(d, device="cuda") % 2 == 0, 1.0, -1.0).to(w.dtype)
+    y = c.decode()
+    torch.cuda.synchronize()
+    assert (y[:, 0::2] == float("inf")).all() and (y[:, 1::2] == -float("inf")).all()

@@ -274,6 +274,23 @@ def test_int_gemm_strides(M, N, K, lda, ldw, ldy, out):
     _check(_run_gemm(q, s, w, t, out, lda, ldw, ldy), _ref_product(q, s, w, t), 4 * U, out)
 
 
+def _tiles(rows, groups, N, cols):
+    """Upper bound on the 128 x `cols` tiles of a product: more than there are SMs run as 256 x 256 pair tiles."""
+    return (rows // 128 + groups) * -(-N // cols)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", [
+    (17, 19500, 16), (20, 19000, 400), (32, 19201, 144), (33, 20001, 272), (64, 19456, 128), (100, 19208, 80), (128, 19600, 64),
+    (129, 9700, 144), (256, 9601, 208), (257, 9001, 144), (300, 8192, 1040), (513, 5000, 272), (1500, 2100, 80), (4100, 1040, 640),
+])
+def test_int_gemm_pair_tiles(M, N, K, out):
+    assert -(-M // 128) * -(-N // 128) > torch.cuda.get_device_properties(0).multi_processor_count
+    q, s, w, t = _problem(M, N, K, M * 7919 + N * 31 + K)
+    _check(_run_gemm(q, s, w, t, out, ldy=N + 3 if M % 2 else N), _ref_product(q, s, w, t), 4 * U, out)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 16, 20, 130, 300])
 def test_int_gemm_largest_sums(M):
@@ -363,19 +380,35 @@ def test_expert_products(counts, N, K, swiglu, out):
 @pytest.mark.gpu
 @pytest.mark.parametrize("out", [F32, BF16])
 @pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("counts,N,K", [
+    ((3, 0, 5, 8, 0, 2), 4096, 256), ((16, 9, 33), 6400, 144), ((64, 1, 63, 65), 5008, 128), ((130, 0, 255, 1), 5000, 512),
+    ((256, 257, 128, 129), 2600, 192), ((700, 3, 0, 20), 2216, 256), ((40, 300, 90), 4005, 208), ((5, 2000), 1300, 144),
+    ((33,) * 20, 1000, 64), ((1, 0, 290, 31, 32, 600), 2056, 272), ((0, 0, 0, 4), 5008, 16),
+])
+def test_expert_products_pair_tiles(counts, N, K, swiglu, out):
+    assert _tiles(sum(counts), len(counts), N, 128) > torch.cuda.get_device_properties(0).multi_processor_count
+    c = _experts_case(counts, N, K, len(counts) * 7 + N + K, swiglu)
+    _check_experts(c, _run_experts(c, out, ldy=N + 5 if K % 32 else None), out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("N", [77, 4077])
 @pytest.mark.parametrize("counts", [(3, 0, 9), (40, 0, 150), (300, 10, 500)])
-def test_expert_products_strides_and_rows_outside(counts, swiglu, out):
+def test_expert_products_strides_and_rows_outside(counts, N, swiglu, out):
     # gaps between experts, padded rows, and rows before the first and behind the last group
-    c = _experts_case(counts, 77, 144, 9, swiglu, before=5, after=70)
-    _check_experts(c, _run_experts(c, out, w_more=48, s_more=5, lda=160, ldy=81), out)
+    c = _experts_case(counts, N, 144, 9, swiglu, before=5, after=70)
+    _check_experts(c, _run_experts(c, out, w_more=48, s_more=5, lda=160, ldy=N + 4), out)
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("N", [64, 6400])
 @pytest.mark.parametrize("scale", [1, 40])
-def test_expert_products_bad_offsets(swiglu, scale):
+def test_expert_products_bad_offsets(swiglu, N, scale):
     # entries out of range or falling: each counts as the largest so far, within [0, rows]
-    c = _experts_case((scale * 5, scale * 7, scale * 4), 64, 128, 4, swiglu)
+    c = _experts_case((scale * 5, scale * 7, scale * 4), N, 128, 4, swiglu)
     bad = torch.tensor([-9, scale * 6, scale * 2, 10 ** 9], dtype=torch.int32)
     seen = torch.cummax(bad.clamp(0, c["R"]), 0).values
     _check_experts(c, _run_experts(c, F32, off=bad), F32, off=seen)
