@@ -51,7 +51,11 @@ struct SkinnyParams {
   int64_t ldw;
   const float* w_scale;
   int64_t ldy;
-  int M, N, K;
+  int M, K, chunks;
+  // CTA i has each + (i < rest) columns, in groups[i < rest] groups of wide columns or, the first `wider`,
+  // one more (divided on the host: the divisions cost the kernel a third of its 1.7 us before the first copy)
+  int each, rest;
+  int groups[2], wide[2], wider[2];
 };
 
 template <int NT, typename Out>
@@ -63,13 +67,16 @@ __global__ void __launch_bounds__(kThreads, 1) i8_skinny_kernel(const SkinnyPara
   pdl_wait();
 
   // this CTA's columns and its groups of nearly equal width
-  const int G = gridDim.x, each = p.N / G, rest = p.N - each * G, i0 = blockIdx.x;
-  const int n0 = each * i0 + min(i0, rest), cols = each + (i0 < rest ? 1 : 0);
-  const int groups = (cols + kGroup - 1) / kGroup, wide = cols / groups, wider = cols - wide * groups;
+  const int i0 = blockIdx.x;
+  const bool more = i0 < p.rest;
+  const int n0 = p.each * i0 + min(i0, p.rest), chunks = p.chunks;
+  const int groups = more ? p.groups[1] : p.groups[0], wide = more ? p.wide[1] : p.wide[0],
+            wider = more ? p.wider[1] : p.wider[0];
   auto first = [&](int i) { return n0 + wide * i + min(i, wider); };
-  const int chunks = (p.K + 63) / 64;
-  // the run of warp w over the chunks of the batch of groups that starts at group b
+  // the run of warp w over the chunks of the batch of groups that starts at group b: where it begins, and
+  // the group of the batch that this lies in
   auto bound = [&](int b, int w) { return min(kBatch, groups - b) * chunks * w / kWarps; };
+  auto group_of = [&](int b, int w) { return min(kBatch, groups - b) * w / kWarps; };
 
   // the stream: chunk `sc` of group `sb` + `si` is copied next; `left` chunks of its run in the batch
   const uint32_t ring = smem_u32(smem) + warp * (kDepth * kStage) + lane * 16;
@@ -82,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_skinny_kernel(const SkinnyPara
       if (sb >= groups) return;
       const int a = bound(sb, warp);
       left = bound(sb, warp + 1) - a;
-      si = a / chunks;
+      si = group_of(sb, warp);
       sc = a - si * chunks;
     }
     const int a = first(sb + si), b = first(sb + si + 1);
@@ -122,8 +129,9 @@ __global__ void __launch_bounds__(kThreads, 1) i8_skinny_kernel(const SkinnyPara
   int slot = 0;
   for (int b = 0; b < groups; b += kBatch) {
     const int end = bound(b, warp + 1);
-    for (int pos = bound(b, warp); pos < end;) {
-      const int i = pos / chunks, ca = pos - i * chunks, cb = min(chunks, ca + end - pos);
+    int i = group_of(b, warp);
+    for (int pos = bound(b, warp); pos < end; ++i) {
+      const int ca = pos - i * chunks, cb = min(chunks, end - i * chunks);
       int acc[2][NT][4] = {};
       uint4 xn[NT];
 #pragma unroll
@@ -167,11 +175,13 @@ __global__ void __launch_bounds__(kThreads, 1) i8_skinny_kernel(const SkinnyPara
     for (int i = 0; warp < p.M && i < nb; ++i) {  // warp = row, lane = column
       const int n = first(b + i) + lane;
       if (n >= first(b + i + 1)) continue;
-      // the warps whose runs hold the group's first and last chunk, and those between
-      const int all = nb * chunks, lo = ((i * chunks + 1) * kWarps - 1) / all, hi = ((i + 1) * chunks * kWarps - 1) / all;
-      int s = 0;
-      for (int w = lo; w <= hi; ++w)
-        if (bound(b, w) < bound(b, w + 1)) s += red[(i + w) * kSlot + lane * kPitch + warp];
+      int s = 0, from = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {  // the warps whose runs have a part in the group
+        const int to = bound(b, w + 1);
+        if (max(from, i * chunks) < min(to, (i + 1) * chunks)) s += red[(i + w) * kSlot + lane * kPitch + warp];
+        from = to;
+      }
       y[warp * p.ldy + n] = from_f32<Out>((float)s * (__ldg(p.a_scale + warp) * __ldg(p.w_scale + n)));
     }
     __syncthreads();
@@ -186,8 +196,15 @@ cudaError_t launch_int_skinny(const IntGemmArgs& a, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const SkinnyParams p{a.A, a.lda, a.a_scale, a.W, a.ldw, a.w_scale, a.ldy, a.rows, a.N, a.K};
-  const dim3 grid(std::min(sms, a.N)), block(kThreads);
+  const int ctas = std::min(sms, a.N);
+  SkinnyParams p{a.A, a.lda, a.a_scale, a.W, a.ldw, a.w_scale, a.ldy, a.rows, a.K, (a.K + 63) / 64, a.N / ctas, a.N % ctas};
+  for (int more = 0; more < 2; ++more) {
+    const int cols = p.each + more;
+    p.groups[more] = (cols + kGroup - 1) / kGroup;
+    p.wide[more] = cols / p.groups[more];
+    p.wider[more] = cols % p.groups[more];
+  }
+  const dim3 grid(ctas), block(kThreads);
   auto launch = [&](auto kern, auto* y) {
     const cudaError_t e2 = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     return e2 != cudaSuccess ? e2 : launch_kernel(kern, grid, block, kSmem, s, 1, p, y);
