@@ -254,6 +254,13 @@ __device__ __forceinline__ void tc_mma_i8_pair(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Arrival that publishes no memory: it frees an accumulator whose values are in registers.  With release
 // semantics it waits for the epilogue's stores to global memory (1.1 us per tile, measured).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
@@ -423,42 +430,46 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA producer (both CTAs)
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      const uint64_t evict_first = l2_evict_first_policy();
-      bool ok = true;
-      int it = 0;
-      for (int L = pair; ok && L < total; L += npairs, ++it) {
-        const int slot = it % kPlans;
-        if (!wait_or_abort(&m.ifull[slot], (uint32_t)(it / kPlans) & 1u, abort_flag)) {
-          raise_abort(m, err);
+    const bool lead = elect_one();
+    int s = 0;
+    uint32_t ph = 0;
+    const uint64_t evict_first = l2_evict_first_policy();
+    const uint32_t full0 = mapa_shared(smem_u32(&m.full[0]), 0);
+    bool ok = true;
+    int it = 0;
+    for (int L = pair; ok && L < total; L += npairs, ++it) {
+      const int slot = it % kPlans;
+      if (!__all_sync(0xffffffffu, wait_or_abort(&m.ifull[slot], (uint32_t)(it / kPlans) & 1u, abort_flag))) {
+        if (lead) raise_abort(m, err);
+        break;
+      }
+      const Tile& ts = m.tile[slot];
+      const int e = __shfl_sync(0xffffffffu, ts.e, 0), row0 = __shfl_sync(0xffffffffu, ts.row0, 0);
+      const int trows = __shfl_sync(0xffffffffu, ts.row_end, 0) - row0, n0 = __shfl_sync(0xffffffffu, ts.n0, 0);
+      const int mtiles = __shfl_sync(0xffffffffu, ts.mtiles, 0);
+      if (lead) mbar_arrive(&m.pfree[slot]);
+      const bool light = trows <= p.light_rows, dense = light && trows <= kDenseRows;
+      const bool once = light && mtiles == 1;  // its weights are read by this tile alone: evict them first
+      const int nh = (trows + 31) / 32 * 16;   // swapped: token rows (N / 2) per CTA
+      const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
+      for (int step = 0; step < steps; ++step) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(&m.empty[s], ph ^ 1u, abort_flag))) {
+          if (lead) raise_abort(m, err);
+          ok = false;
           break;
         }
-        const Tile t = m.tile[slot];
-        mbar_arrive(&m.pfree[slot]);
-        const int trows = t.row_end - t.row0;
-        const bool light = trows <= p.light_rows, dense = light && trows <= kDenseRows;
-        const bool once = light && t.mtiles == 1;  // its weights are read by this tile alone: evict them first
-        const int nh = (trows + 31) / 32 * 16;     // swapped: token rows (N / 2) per CTA
-        const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
-        for (int step = 0; step < steps; ++step) {
-          if (!wait_or_abort(&m.empty[s], ph ^ 1u, abort_flag)) {
-            raise_abort(m, err);
-            ok = false;
-            break;
-          }
+        if (lead) {
           uint8_t* sA = smem + (size_t)s * kStage;
           uint8_t* sB = sA + kHalf;
-          const uint32_t bar = mapa_shared(smem_u32(&m.full[s]), 0);
+          const uint32_t bar = full0 + (uint32_t)s * 8u;
           // 128 weight rows of a swapped tile
           auto weights = [&](uint8_t* dst, int kx) {
             if (kSwiglu) {
-              if (once) tma2_load_5d_hint(dst, &p.mapB16, bar, kx, 0, 0, (t.n0 + 64 * (int)rank) / 16, t.e, evict_first);
-              else tma2_load_5d(dst, &p.mapB16, bar, kx, 0, 0, (t.n0 + 64 * (int)rank) / 16, t.e);
+              if (once) tma2_load_5d_hint(dst, &p.mapB16, bar, kx, 0, 0, (n0 + 64 * (int)rank) / 16, e, evict_first);
+              else tma2_load_5d(dst, &p.mapB16, bar, kx, 0, 0, (n0 + 64 * (int)rank) / 16, e);
             } else {
-              if (once) tma2_load_3d_hint(dst, &p.mapB, bar, kx, t.n0 + 128 * (int)rank, t.e, evict_first);
-              else tma2_load_3d(dst, &p.mapB, bar, kx, t.n0 + 128 * (int)rank, t.e);
+              if (once) tma2_load_3d_hint(dst, &p.mapB, bar, kx, n0 + 128 * (int)rank, e, evict_first);
+              else tma2_load_3d(dst, &p.mapB, bar, kx, n0 + 128 * (int)rank, e);
             }
           };
           if (dense) {
@@ -467,23 +478,24 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
             for (int j = 0; j < nk; ++j) {
               const int kx = (2 * step + j) * kKB;
               weights(sA + (size_t)j * kHalf, kx);
-              tma2_load_2d(tok_base + (size_t)(2 * s + j) * kTok, &p.mapA16, bar, kx, t.row0 + (int)rank * nh);
+              tma2_load_2d(tok_base + (size_t)(2 * s + j) * kTok, &p.mapA16, bar, kx, row0 + (int)rank * nh);
             }
           } else if (light) {
             const int box = nh <= 32 ? 32 : 64;
             if (rank == 0) mbar_arrive_expect_tx(&m.full[s], (uint32_t)(2 * (kHalf + box * kKB)));
             weights(sA, step * kKB);
-            tma2_load_2d(sB, nh <= 32 ? &p.mapA32 : &p.mapA64, bar, step * kKB, t.row0 + (int)rank * nh);
+            tma2_load_2d(sB, nh <= 32 ? &p.mapA32 : &p.mapA64, bar, step * kKB, row0 + (int)rank * nh);
           } else {
             if (rank == 0) mbar_arrive_expect_tx(&m.full[s], 2 * kStage);
-            tma2_load_2d(sA, &p.mapA, bar, step * kKB, t.row0 + 128 * (int)rank);
-            if (kSwiglu) tma2_load_4d(sB, &p.mapB, bar, step * kKB, t.n0, (int)rank, t.e);
-            else tma2_load_3d(sB, &p.mapB, bar, step * kKB, t.n0 + 128 * (int)rank, t.e);
+            tma2_load_2d(sA, &p.mapA, bar, step * kKB, row0 + 128 * (int)rank);
+            if (kSwiglu) tma2_load_4d(sB, &p.mapB, bar, step * kKB, n0, (int)rank, e);
+            else tma2_load_3d(sB, &p.mapB, bar, step * kKB, n0 + 128 * (int)rank, e);
           }
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
         }
       }
     }
@@ -491,62 +503,67 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer (leader only)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool lead = elect_one();
       int s = 0, it = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int L = pair; ok && L < total; L += npairs, ++it) {
         const int slot = it % kPlans;
-        if (!wait_or_abort(&m.ifull[slot], (uint32_t)(it / kPlans) & 1u, abort_flag)) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(&m.ifull[slot], (uint32_t)(it / kPlans) & 1u, abort_flag))) {
           ok = false;
           break;
         }
-        const Tile t = m.tile[slot];
-        mbar_arrive(&m.pfree[slot]);
+        const int trows = __shfl_sync(0xffffffffu, m.tile[slot].row_end - m.tile[slot].row0, 0);
+        if (lead) mbar_arrive(&m.pfree[slot]);
         const int a = it & 1;
-        if (!wait_or_abort(&m.tempty[a], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag)) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(&m.tempty[a], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(a * kBN);
-        const int trows = t.row_end - t.row0;
         const bool light = trows <= p.light_rows, dense = light && trows <= kDenseRows;
         const uint32_t idesc = light ? idesc_s8_s32(kBM, (trows + 31) / 32 * 32) : idesc_s8_s32(kBM, kBN);
         const int steps = dense ? (p.num_kb + 1) / 2 : p.num_kb;
         for (int step = 0; step < steps; ++step) {
-          if (!wait_or_abort(&m.full[s], ph, abort_flag)) {
+          if (!__all_sync(0xffffffffu, wait_or_abort(&m.full[s], ph, abort_flag))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sA = smem_u32(smem + (size_t)s * kStage);
-          if (dense) {
-            const int nk = min(2, p.num_kb - 2 * step);
-            for (int j = 0; j < nk; ++j) {
-              const uint32_t wa = sA + (uint32_t)(j * kHalf), tb = smem_u32(tok_base + (size_t)(2 * s + j) * kTok);
+          const uint32_t sA = smem_u32(smem) + (uint32_t)s * kStage;
+          if (lead) {
+            if (dense) {
+              const int nk = min(2, p.num_kb - 2 * step);
+              for (int j = 0; j < nk; ++j) {
+                const uint64_t wa = smem_desc_sw128(sA + (uint32_t)(j * kHalf));
+                const uint64_t tb = smem_desc_sw128(smem_u32(tok_base) + (uint32_t)(2 * s + j) * kTok);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_i8_pair(d_tmem, smem_desc_sw128(wa + kk * 32), smem_desc_sw128(tb + kk * 32), idesc,
-                               (step | j | kk) != 0 ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_i8_pair(d_tmem, wa + 2 * kk, tb + 2 * kk, idesc, (step | j | kk) != 0 ? 1u : 0u);
+              }
+            } else {
+              const uint64_t da = smem_desc_sw128(sA), db = smem_desc_sw128(sA + kHalf);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) tc_mma_i8_pair(d_tmem, da + 2 * kk, db + 2 * kk, idesc, (step | kk) != 0 ? 1u : 0u);
             }
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_i8_pair(d_tmem, smem_desc_sw128(sA + kk * 32), smem_desc_sw128(sA + kHalf + kk * 32), idesc,
-                             (step | kk) != 0 ? 1u : 0u);
+            tc_commit_pair_mc(&m.empty[s], 0x3);
           }
-          tc_commit_pair_mc(&m.empty[s], 0x3);
+          __syncwarp();
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
           }
         }
-        if (ok) tc_commit_pair_mc(&m.tfull[a], 0x3);
+        if (ok && lead) tc_commit_pair_mc(&m.tfull[a], 0x3);
+        __syncwarp();
       }
-      if (!ok) raise_abort(m, err);
-      tc_commit_pair(&m.drain);
-      mbar_wait_bounded(&m.drain, 0);
+      if (lead) {
+        if (!ok) raise_abort(m, err);
+        tc_commit_pair(&m.drain);
+        mbar_wait_bounded(&m.drain, 0);
+      }
     }
     __syncwarp();
   } else if (warp == 2 + kEpiWarps) {
@@ -801,14 +818,15 @@ __global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid
   const int kb0 = p.num_kb * rank / S, kb1 = p.num_kb * (rank + 1) / S;  // this CTA's k blocks
 
   if (work && warp == 0) {
-    if (lane == 0) {
-      int issued = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
-        const int s = issued % kSplitStages;
-        if (!wait_or_abort(&m.empty[s], ((uint32_t)(issued / kSplitStages) & 1u) ^ 1u, abort_flag)) {
-          raise_abort(m, err);
-          break;
-        }
+    const bool lead = elect_one();
+    int issued = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+      const int s = issued % kSplitStages;
+      if (!__all_sync(0xffffffffu, wait_or_abort(&m.empty[s], ((uint32_t)(issued / kSplitStages) & 1u) ^ 1u, abort_flag))) {
+        if (lead) raise_abort(m, err);
+        break;
+      }
+      if (lead) {
         uint8_t* sA = smem + (size_t)s * kStage;
         uint8_t* sB = sA + kHalf;
         mbar_arrive_expect_tx(&m.full[s], kStage);
@@ -820,26 +838,31 @@ __global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid
           tma_load_3d(sB, &p.mapB, &m.full[s], kb * kKB, t.n0, t.e);
         }
       }
-      m.issued = issued;
+      __syncwarp();
     }
-    __syncwarp();
+    if (lead) m.issued = issued;
   } else if (work && warp == 1) {
-    if (lane == 0) {
-      int consumed = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++consumed) {
-        const int s = consumed % kSplitStages;
-        if (!wait_or_abort(&m.full[s], (uint32_t)(consumed / kSplitStages) & 1u, abort_flag)) {
-          raise_abort(m, err);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sA = smem_u32(smem + (size_t)s * kStage);
+    const bool lead = elect_one();
+    int consumed = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++consumed) {
+      const int s = consumed % kSplitStages;
+      if (!__all_sync(0xffffffffu, wait_or_abort(&m.full[s], (uint32_t)(consumed / kSplitStages) & 1u, abort_flag))) {
+        if (lead) raise_abort(m, err);
+        break;
+      }
+      tc_fence_after();
+      if (lead) {
+        const uint64_t da = smem_desc_sw128(smem_u32(smem) + (uint32_t)s * kStage);
+        const uint64_t db = smem_desc_sw128(smem_u32(smem) + (uint32_t)s * kStage + kHalf);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          tc_mma_i8(tmem_base, smem_desc_sw128(sA + kk * 32), smem_desc_sw128(sA + kHalf + kk * 32),
-                    idesc_s8_s32(kSplitTile, kSplitTile), (consumed | kk) != 0 ? 1u : 0u);
+          tc_mma_i8(tmem_base, da + 2 * kk, db + 2 * kk, idesc_s8_s32(kSplitTile, kSplitTile),
+                    (consumed | kk) != 0 ? 1u : 0u);
         tc_commit(&m.empty[s]);
       }
+      __syncwarp();
+    }
+    if (lead) {
       m.consumed = consumed;
       tc_commit(&m.tfull);  // also after an error: every MMA issued has ended
       mbar_wait_bounded(&m.tfull, 0);
