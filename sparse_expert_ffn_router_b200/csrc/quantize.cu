@@ -13,12 +13,12 @@
 //
 // A row whose s would be below 2^-126 (all zeros, or nothing above 127 * 2^-126) gets s = 1 and
 // zeros.  A row that holds a NaN or an infinity gets s = NaN and zeros: every product with it is
-// then NaN, as the row's own values would have made it.
+// then NaN.
 //
 // Bound by memory: a row is read once, kept in registers while its maximum is formed, and written
-// once (3 bytes per bf16 element).  Each thread owns units of 16 elements (two or four 16-byte
+// once (3 bytes per bf16 element); the next row is on its way meanwhile.  Each thread owns units of 16 elements (two or four 16-byte
 // loads, one 16-byte store).  Measured (B200): 16384 x 16384 bf16 142 us = 5.7 TB/s, fp32 195 us = 6.9 TB/s;
-// 4096 x 4096 bf16 16.5 us = 3.1 TB/s, two waves of latency (21 us with the comparison made for every
+// 4096 x 4096 bf16 14.7 us = 3.4 TB/s, launch and latency among it (21 us with the comparison made for every
 // value).
 #include <algorithm>
 
@@ -107,15 +107,29 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 3 : 2) quantize_ro
   constexpr int kRows = kQThreads / TPR;
   __shared__ uint32_t part[kQThreads / 32];
   const int t = threadIdx.x % TPR;
-  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
+  constexpr bool kAhead = kQUnits <= 2;  // the next row is loaded while this one is rounded
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  Unit16<T> next[kAhead ? kQUnits : 1];
+  auto fetch = [&](Unit16<T>* v, int64_t r) {
+    const T* src = x + (r < rows ? r : 0) * ldx;
+#pragma unroll
+    for (int i = 0; i < kQUnits; ++i)
+      if (r < rows && t + i * TPR < units) v[i].load(src + (size_t)(t + i * TPR) * 16);
+  };
+  if (kAhead) fetch(next, (int64_t)blockIdx.x * kRows + threadIdx.x / TPR);
+  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += step) {
     const int64_t r = r0 + threadIdx.x / TPR;
     const bool live = r < rows;
     const T* src = x + (live ? r : 0) * ldx;
     Unit16<T> u[kQUnits];
     uint32_t top = 0;
+    if (kAhead) {
 #pragma unroll
-    for (int i = 0; i < kQUnits; ++i)
-      if (live && t + i * TPR < units) u[i].load(src + (size_t)(t + i * TPR) * 16);
+      for (int i = 0; i < kQUnits; ++i) u[i] = next[kAhead ? i : 0];
+      fetch(next, r + step);
+    } else {
+      fetch(u, r);
+    }
 #pragma unroll
     for (int i = 0; i < kQUnits; ++i)
       if (live && t + i * TPR < units) top = max(top, unit_top(u[i]));
@@ -173,22 +187,25 @@ template <typename T, int TPR, int kQUnits>
 cudaError_t launch_q(const T* x, int rows, int units, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
                      const int32_t* dst, int k, cudaStream_t s) {
   constexpr int kRows = kQThreads / TPR;
-  const int grid = std::min((rows + kRows - 1) / kRows, 148 * 64);
+  // rows loaded ahead: the CTAs that fit on the GPU at once go round (else a CTA takes few rows)
+  const int most = kQUnits <= 2 ? 148 * (sizeof(T) == 2 ? 3 : 2) : 148 * 64;
+  const int grid = std::min((rows + kRows - 1) / kRows, most);
   return launch_kernel(quantize_rows_kernel<T, TPR, kQUnits>, dim3(grid), dim3(kQThreads), 0, s, 1, x, rows, units, ldx,
                        q, ldq, scale, dst, k);
 }
 
-// The fewest threads per row that hold it in four units each, so that a thread has several loads in
-// flight (4096 x 4096 bf16: 27 us with one unit on each of 256 threads).
+// The fewest threads per row that hold it in two units each, so that the next row's two fit beside them
+// (4096 x 4096 bf16: 16.3 us with four units and no row ahead, 19.3 with four and a row ahead, which
+// spills); longer rows four units on 256 threads.
 template <typename T>
 cudaError_t launch_rows(const T* x, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
                         const int32_t* dst, int k, cudaStream_t s) {
   const int units = cols / 16;
   if (units <= 32) return launch_q<T, 32, 1>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
   if (units <= 64) return launch_q<T, 32, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
-  if (units <= 128) return launch_q<T, 32, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
-  if (units <= 256) return launch_q<T, 64, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
-  if (units <= 512) return launch_q<T, 128, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
+  if (units <= 128) return launch_q<T, 64, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
+  if (units <= 256) return launch_q<T, 128, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
+  if (units <= 512) return launch_q<T, 256, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
   return launch_q<T, 256, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
 }
 
