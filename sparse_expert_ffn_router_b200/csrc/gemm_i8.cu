@@ -19,28 +19,31 @@
 //               roles themselves this cost 1.5 us between two tiles of MMAs and 3 us per epilogue)
 // A group's last m-tile of at most 128 rows runs with the operands swapped (weights the M side, its
 // rows rounded up to 32 the N side), so that a group of a few rows costs the stream of its weights
-// and little else; with at most 32 rows a stage holds two k blocks of weights.  For SwiGLU a swapped
+// and little else; with at most 32 rows a stage holds two k blocks of weights (one: skewed experts 154 -> 163 us).  For SwiGLU a swapped
 // tile's 128 weight rows per CTA are 4 x (16 of W1, the same 16 of W3), so that gate and up of a
 // column meet in one warp; that needs N to be a multiple of 16, other N take the full tile.
 // Tiles are numbered group-major, then n-tile, then m-tile fastest, so that the pairs running together
 // share weight tiles through L2; groups of a single m-tile (streams of weights) are interleaved with
 // the others in proportion.  Pair i takes tiles i, i + pairs, ...
 //
+// The producer's and the MMA warp's loops run converged and one elected lane issues (under a branch on the
+// lane number the compiler moves every operand to the uniform registers in turn: 0.1 us per copy, 0.05 us
+// per MMA, so that a stage took 0.31 us whatever it held).
+//
 // What bounds a full tile: a stage of 64 KB per pair feeds 512 cycles of MMAs (8192 multiply-adds per
-// cycle and SM) and takes 0.37-0.44 us, against 0.28 us for the MMAs alone at 1.81 GHz: the MMAs read 64
-// bytes of shared memory per cycle and SM while the copies write 64, which is all that one SM's shared
-// memory has.  Measured (B200): 4096 x 14336 x 4096 164 us = 2.9 POP/s, the tensor pipe busy 69 % of the time,
-// 1.9 GB from L2; rows of 8 experts times [2 x 14336, 4096] with SwiGLU 694 us = 2.8 POP/s (830 us when
-// it runs without a pause under the power cap); 64 rows on 8 experts (940 MB of weights) 148 us = 6.4 TB/s.
-// With little k per tile the epilogue bounds it (1.9 us per 256 x 256 tile).
+// cycle and SM), 0.26 us; one pair alone takes 0.28 us, all of them 0.36 us: 13 TB/s from L2 to the SMs,
+// with 160 KB in flight per SM (4 stages: 157 us where 5 take 150, 3: 179).  Measured (B200):
+// 4096 x 14336 x 4096 150 us = 3.2 POP/s; rows of 8 experts times [2 x 14336, 4096] with SwiGLU 631 us = 3.05 POP/s
+// (766 us when it runs without a pause under the power cap); 64 rows on 8 experts (940 MB of weights)
+// 142 us = 6.6 TB/s.  With little k per tile the epilogue bounds it (1.9 us per 256 x 256 tile).
 //
 // i8_split_kernel: products of too few pair tiles to occupy the GPU.  Tiles of 128 x 128 (one CTA each,
 // cta_group::1) whose k range is split over the S = 1, 2 or 4 CTAs of a cluster; the int32 partial
 // sums, exact in any order, are exchanged through the cluster's shared memory (the idle ring), each
 // CTA finishing 1 / S of the columns.  What bounds such a product is the feed of one SM's shared
 // memory (about 100 GB/s measured, against 43 GB/s of HBM per SM), so the SMs left idle are worth more
-// than the larger tile: 4096 x 4096 at 128 rows 12.5 us against 19.4 as pair tiles, 4096 x 14336 at 64 rows
-// 18.6 against 43; 14336 x 4096 at 256 rows has 224 such tiles and stays with the pairs (21 us).
+// than the larger tile: 4096 x 4096 at 128 rows 12.5 us against 17.1 as pair tiles, 4096 x 14336 at 64 rows
+// 16.7 against 33.9; 14336 x 4096 at 256 rows has 224 such tiles and stays with the pairs (18.7 us).
 //
 // Every wait is bounded (kWaitTimeoutNs); one that gives up sets the error word and ends all roles.
 #include <algorithm>
@@ -1057,7 +1060,10 @@ cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // Fewer tiles of 128 x 128 than SMs: one CTA per tile, or with k split 2 or 4 CTAs, all at once;
-  // more tiles keep the pair kernel's SMs busy (both sides: the header comment).
+  // more tiles keep the pair kernel's SMs busy (both sides: the header comment).  With at most 32 rows the
+  // pair kernel streams two k blocks of weights per stage and is ahead too, unless four CTAs share a
+  // long k (32 rows, weights from HBM: 14336 x 4096 20.7 against 24.0 us, 8192 x 4096 18.2 / 20.2, 4096 x 5120
+  // 16.7 / 18.4, but 2048 x 8192 20.6 / 18.3, 4096 x 14336 28.8 / 26.6).
   const int groups = a.offsets ? a.E : 1, cols = swiglu ? kSplitTile / 2 : kSplitTile;
   const long long tiles = (a.offsets ? (long long)a.rows / kSplitTile + groups : (a.rows + kSplitTile - 1) / kSplitTile) *
                           ((a.N + cols - 1) / cols);
@@ -1065,7 +1071,9 @@ cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s) {
     const int kbs = (a.K + kKB - 1) / kKB;
     int split = 1;
     while (split < kSplitMax && tiles * split * 2 <= sms && kbs >= 4 * split) split *= 2;
-    return swiglu ? launch_split<true>(a, (int)tiles, split, s) : launch_split<false>(a, (int)tiles, split, s);
+    const bool swapped = a.rows <= kDenseRows && (!swiglu || a.N % 16 == 0);
+    if (!swapped || (split == kSplitMax && kbs > 40))
+      return swiglu ? launch_split<true>(a, (int)tiles, split, s) : launch_split<false>(a, (int)tiles, split, s);
   }
   return swiglu ? launch_pair<true>(a, sms, s) : launch_pair<false>(a, sms, s);
 }

@@ -292,6 +292,18 @@ def test_int_gemm_pair_tiles(M, N, K, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", [
+    (17, 1, 16), (17, 128, 5120), (18, 129, 5136), (24, 300, 5104), (25, 257, 5264), (31, 2049, 144), (32, 10000, 272),
+    (32, 1030, 8208), (33, 1030, 8208), (33, 129, 5120),
+])
+def test_int_gemm_few_rows(M, N, K, out):
+    # 17 to 33 rows, where the kind of tile depends on K
+    q, s, w, t = _problem(M, N, K, M * 131 + N + K)
+    _check(_run_gemm(q, s, w, t, out, ldy=N + 3), _ref_product(q, s, w, t), 4 * U, out)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 16, 20, 130, 300])
 def test_int_gemm_largest_sums(M):
     # every product at its largest: K * 2^14 just below 2^31
@@ -389,6 +401,16 @@ def test_expert_products_pair_tiles(counts, N, K, swiglu, out):
     assert _tiles(sum(counts), len(counts), N, 128) > torch.cuda.get_device_properties(0).multi_processor_count
     c = _experts_case(counts, N, K, len(counts) * 7 + N + K, swiglu)
     _check_experts(c, _run_experts(c, out, ldy=N + 5 if K % 32 else None), out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("N", [77, 80, 1000, 1008])
+@pytest.mark.parametrize("counts,K", [((1, 0, 16, 15), 5120), ((1, 0, 16, 15), 5136), ((32,), 5200), ((2, 30, 1), 5136), ((0, 1), 144)])
+def test_expert_products_few_rows(counts, K, N, swiglu, out):
+    c = _experts_case(counts, N, K, len(counts) * 13 + N + K, swiglu)
+    _check_experts(c, _run_experts(c, out, ldy=N + 5), out)
 
 
 @pytest.mark.gpu
