@@ -416,7 +416,7 @@ struct IntGemmArgs {
   uint32_t* err;           // error word of bounded waits, or nullptr: the library's own word per device
 };
 constexpr int kSkinnyRows = 16;  // one group of at most this many rows: gemv_i8.cu
-cudaError_t launch_int_skinny(const IntGemmArgs& a, cudaStream_t s);
+cudaError_t launch_int_skinny(const IntGemmArgs& a, int sms, cudaStream_t s);
 cudaError_t int_gemm_take_error(uint32_t* word);  // reads and clears the current device's own word
 cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s);
 // dst: nullptr, or [rows, k]: row r's integers and scale go to rows dst[r][0..k) instead of to row r

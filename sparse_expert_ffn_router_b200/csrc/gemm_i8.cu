@@ -1054,11 +1054,18 @@ cudaError_t launch_split(const IntGemmArgs& a, int tiles, int split, cudaStream_
 
 cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s) {
   if (a.rows <= 0) return cudaSuccess;
-  if (!swiglu && !a.offsets && a.rows <= kSkinnyRows) return launch_int_skinny(a, s);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  // At most 16 rows of one product: the stream of gemv_i8.cu, until the weights are so many that the pair
+  // kernel's copies, with a tile for at least half its pairs, make up for its set-up.  Weights from HBM,
+  // there and here: 1 row of 9728 x 4096 16.4 / 18.0 us, 14336 x 4096 22.6 / 20.4, 152000 x 1024 55 / 38;
+  // 16 rows of 16384 x 2048 18.5 / 16.4, 14336 x 4096 24.5 / 20.4, 152000 x 1024 61 / 39 (with 14336 x 4096
+  // in L2 10.4 / 13 at 1 row and 14.1 / 13 at 16).
+  if (!swiglu && !a.offsets && a.rows <= kSkinnyRows &&
+      ((a.N + kBN - 1) / kBN <= sms / 4 || (int64_t)a.N * a.K < (a.rows <= 8 ? 5 : 4) * (int64_t(1) << 23)))
+    return launch_int_skinny(a, sms, s);
   // Fewer tiles of 128 x 128 than SMs: one CTA per tile, or with k split 2 or 4 CTAs, all at once;
   // more tiles keep the pair kernel's SMs busy (both sides: the header comment).  With at most 32 rows the
   // pair kernel streams two k blocks of weights per stage and is ahead too, unless four CTAs share a

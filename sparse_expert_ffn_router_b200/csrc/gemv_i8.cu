@@ -5,16 +5,17 @@
 // Every weight byte is read once and meets a few rows, so the work is a stream over the weights and the
 // bound is HBM (or, for a small product, the latency of one round trip).  Each CTA owns an equal share
 // of the output columns, in groups of at most 32; the groups' chunks of 64 bytes of k, laid end to
-// end, go to its 16 warps in equal runs.  A lane keeps 4 weight rows x 4 chunks of 16 bytes in flight in a ring of shared memory that the same
-// lane fills (cp.async) and drains, so the ring needs no barrier and runs ahead into the next group.
+// end, go to its 16 warps in equal runs.  A lane keeps 4 weight rows x 4 chunks of 16 bytes in flight in a
+// ring of shared memory that the same lane fills (cp.async) and drains, so the ring needs no barrier and
+// runs ahead into the next group.
 // The products are mma.m16n8k32 on int8 with the weights as the 16-row operand and the rows as its 8
 // columns: the order of k within an instruction is free, so 16 bytes of a weight row and of a token row
 // feed two instructions as they are.  Sums are exact int32; the warps' parts meet in shared memory once
-// per 8 groups (meeting after each group: 14336 x 4096 at 13 rows 15.7 us).
-// Measured (B200): 4096 x 4096 at one row 6.5 us (14.5 us as a tcgen05 tile: 16 column tiles keep 32 SMs
-// busy); 14336 x 4096 (59 MB) 12.4 us at one row = 4.7 TB/s, 14.6 us at 16 rows (20.4 us with a cold L2).
-// From 17 rows on the tcgen05 tiles take over: 4096 x 4096 at 16 rows 8.3 us here, at 17 rows 12.5 us there,
-// where it stays up to 128 rows.
+// per 8 groups (meeting after each group: 14336 x 4096 at 13 rows 15.7 us against 14.4).
+// Measured (B200), weights in L2 / from HBM: 4096 x 4096 at one row 6.4 / 12.2 us (12.6 / 16.1 as tcgen05
+// tiles: 16 column tiles keep 32 SMs busy), at 16 rows 6.4 / 12.3 (12.6 / 16.3); 4096 x 14336 at 16 rows
+// 12.5 / 22.6 (24.6 as tiles); 1024 x 1024 4.3 / 8.2.  Weights from HBM end up 4 us behind a bare read of
+// the same bytes (18.5 us for 58 MB), so that wide products leave this kernel (launch_int_gemm).
 #include <algorithm>
 
 #include "common.cuh"
@@ -191,11 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_skinny_kernel(const SkinnyPara
 
 }  // namespace
 
-cudaError_t launch_int_skinny(const IntGemmArgs& a, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_int_skinny(const IntGemmArgs& a, int sms, cudaStream_t s) {
   const int ctas = std::min(sms, a.N);
   SkinnyParams p{a.A, a.lda, a.a_scale, a.W, a.ldw, a.w_scale, a.ldy, a.rows, a.K, (a.K + 63) / 64, a.N / ctas, a.N % ctas};
   for (int more = 0; more < 2; ++more) {

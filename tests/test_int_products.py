@@ -304,6 +304,18 @@ def test_int_gemm_few_rows(M, N, K, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 40001, 48), (16, 80003, 16), (5, 39000, 528), (1, 9472, 4432), (8, 9500, 4416), (8, 9500, 4400), (9, 14337, 2352),
+    (9, 14337, 2336), (16, 100001, 336),
+])
+def test_int_gemm_many_columns(M, N, K, out):
+    # at most 16 rows, where the kernel depends on the weights' shape; many groups of columns per block
+    q, s, w, t = _problem(M, N, K, M * 131 + N + K)
+    _check(_run_gemm(q, s, w, t, out, ldy=N + 1), _ref_product(q, s, w, t), 4 * U, out)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 16, 20, 130, 300])
 def test_int_gemm_largest_sums(M):
     # every product at its largest: K * 2^14 just below 2^31
