@@ -30,12 +30,13 @@
 // lane number the compiler moves every operand to the uniform registers in turn: 0.1 us per copy, 0.05 us
 // per MMA, so that a stage took 0.31 us whatever it held).
 //
-// What bounds a full tile: a stage of 64 KB per pair feeds 512 cycles of MMAs (8192 multiply-adds per
-// cycle and SM), 0.26 us; one pair alone takes 0.28 us, all of them 0.36 us: 13 TB/s from L2 to the SMs,
-// with 160 KB in flight per SM (4 stages: 157 us where 5 take 150, 3: 179).  Measured (B200):
-// 4096 x 14336 x 4096 150 us = 3.2 POP/s; rows of 8 experts times [2 x 14336, 4096] with SwiGLU 631 us = 3.05 POP/s
-// (766 us when it runs without a pause under the power cap); 64 rows on 8 experts (940 MB of weights)
-// 142 us = 6.6 TB/s.  With little k per tile the epilogue bounds it (1.9 us per 256 x 256 tile).
+// What bounds a full tile: the MMAs.  A stage of 64 KB per pair feeds 512 cycles of them (8192 multiply-adds
+// per cycle and SM); with all pairs at work it takes 0.36 us at the 1.6 GHz that the power limit leaves, the
+// tensor pipe 89 % busy (82 % of the launch: 12.1 rounds of tiles take 13).  160 KB in flight per SM are
+// just enough (4 stages: 157 us where 5 take 150; 3: 179).  Measured (B200): 4096 x 14336 x 4096 150 us =
+// 3.2 POP/s; rows of 8 experts times [2 x 14336, 4096] with SwiGLU 631 us = 3.05 POP/s (766 us without a
+// pause between calls, the clock lower still); 64 rows on 8 experts (940 MB of weights) 142 us = 6.6 TB/s.
+// With little k per tile the epilogue bounds it (1.9 us per 256 x 256 tile).
 //
 // i8_split_kernel: products of too few pair tiles to occupy the GPU.  Tiles of 128 x 128 (one CTA each,
 // cta_group::1) whose k range is split over the S = 1, 2 or 4 CTAs of a cluster; the int32 partial
