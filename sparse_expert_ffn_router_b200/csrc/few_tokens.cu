@@ -39,8 +39,9 @@
 //
 // Measured (B200, copy bandwidth 6455 GB/s): d = 4096, f = 14336, 8 experts, top-2, bf16: 1 token (704 MB)
 // 120 us, 5.9 TB/s; 16 tokens (2.8 GB) 461 us, 6.1 TB/s.  128 experts of d = 2048, f = 768, top-4, with a
-// shared expert of 1536: 8 tokens (291 MB) 69 us.  A layer of 256 x 512: 18.5 us, latency alone
-// (logits 2.5, selection 1.8, gate/up 5, down 2, the barriers 2 each, the launch 3).
+// shared expert of 1536: 8 tokens (291 MB) 69 us.  An fp32 layer of 256 x 512: 16.5 us, latency alone
+// (logits 2.5, selection 1.8, gate/up 4, down 2, the barriers 2 each, the launch 3).  fp32 with many tokens
+// is bound by the lanes' exchanges and FMAs: two experts of 1024 x 2688 (66 MB) 24 us at one token, 64 at 16.
 #include "common.cuh"
 
 namespace colibri {
@@ -294,7 +295,7 @@ struct FewAcc<__nv_bfloat16, NT> {
         for (int i = 0; i < 4; ++i) v[m][j][i] = 0.f;
   }
   // row q * 8 + g of the tile, token columns 8 j + 2 t and the next
-  __device__ __forceinline__ void store(float* red, int lane) {
+  __device__ __forceinline__ void store(float* red, int, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -334,33 +335,39 @@ struct FewAcc<float, NT> {
 #pragma unroll
       for (int j = 0; j < 8 * NT; ++j) v[q][j] = 0.f;
   }
-  __device__ __forceinline__ void store(float* red, int lane) {
+  // The sum over the row's four lanes of column j0 + t, for lane t: each step hands half of the columns
+  // over (3 exchanges per 4 columns; all columns in all lanes take 8).
+  __device__ __forceinline__ float column(int q, int j0, int t) const {
+    const float* a = v[q] + j0;
+    const bool hi = t & 2, odd = t & 1;
+    const float k0 = (hi ? a[2] : a[0]) + __shfl_xor_sync(0xffffffffu, hi ? a[0] : a[2], 2);
+    const float k1 = (hi ? a[3] : a[1]) + __shfl_xor_sync(0xffffffffu, hi ? a[1] : a[3], 2);
+    return (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
+  }
+  __device__ __forceinline__ void store(float* red, int n, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int j0 = 0; j0 < 8 * NT; j0 += 4) {
+      if (j0 >= n) break;
 #pragma unroll
-      for (int j = 0; j < 8 * NT; ++j) {
-        v[q][j] += __shfl_xor_sync(0xffffffffu, v[q][j], 1);
-        v[q][j] += __shfl_xor_sync(0xffffffffu, v[q][j], 2);
-        if ((j & 3) == t) red[(q * 8 + g) * kFewPitch + j] = v[q][j];
-      }
+      for (int q = 0; q < 4; ++q) red[(q * 8 + g) * kFewPitch + j0 + t] = column(q, j0, t);
+    }
   }
   __device__ __forceinline__ void add(float* red, const uint8_t* tok, const float* w, int n, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int j = 0; j < 8 * NT; ++j)
-      if (j < n) {
+    for (int j0 = 0; j0 < 8 * NT; j0 += 4) {
+      if (j0 >= n) break;
+      const bool own = j0 + t < n;
+      const int to = own ? tok[j0 + t] : 0;
+      const float wt = own ? w[to] : 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x = v[q][j];
-          x += __shfl_xor_sync(0xffffffffu, x, 1);
-          x += __shfl_xor_sync(0xffffffffu, x, 2);
-          if ((j & 3) == t) {
-            float* d = red + (q * 8 + g) * kFewPitch + tok[j];
-            *d = fmaf(w[tok[j]], x, *d);
-          }
-        }
+      for (int q = 0; q < 4; ++q) {
+        const float x = column(q, j0, t);
+        float* d = red + (q * 8 + g) * kFewPitch + to;
+        if (own) *d = fmaf(wt, x, *d);
       }
+    }
   }
 };
 
@@ -428,23 +435,33 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
             mma_bf16(acc.v[m][j], wq[2 * m].z, wq[2 * m + 1].z, wq[2 * m].w, wq[2 * m + 1].w, x.z, x.w);
           }
     } else {
-      // every lane needs every column's bytes: they come from the lane that loaded them
+      // every lane needs every column's bytes: they come from the lane that loaded them, J columns at a
+      // time (zeros beyond the last; with four at a time one token of 4 x 1024 x 2688 took 29 us, not 23)
+      constexpr int J = NT;
 #pragma unroll
-      for (int j = 0; j < 8 * NT; ++j) {
-        if (j >= ncol) continue;
-        const uint4& x = xb[0][j >> 3];
-        float xs[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+      for (int j0 = 0; j0 < 8 * NT; j0 += J) {
+        if (j0 >= ncol) break;
+        const uint4& x = xb[0][j0 >> 3];
+        float xs[J][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) xs[k] = __shfl_sync(0xffffffffu, xs[k], (j & 7) * 4 + t);
+        for (int j = 0; j < J; ++j) {
+          const int from_lane = ((j0 + j) & 7) * 4 + t;
+          xs[j][0] = __shfl_sync(0xffffffffu, __uint_as_float(x.x), from_lane);
+          xs[j][1] = __shfl_sync(0xffffffffu, __uint_as_float(x.y), from_lane);
+          xs[j][2] = __shfl_sync(0xffffffffu, __uint_as_float(x.z), from_lane);
+          xs[j][3] = __shfl_sync(0xffffffffu, __uint_as_float(x.w), from_lane);
+        }
         // four products first, then one addition to the long sum: a quarter of its roundings
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float four = xs[0] * __uint_as_float(wq[q].x);
-          four = fmaf(xs[1], __uint_as_float(wq[q].y), four);
-          four = fmaf(xs[2], __uint_as_float(wq[q].z), four);
-          four = fmaf(xs[3], __uint_as_float(wq[q].w), four);
-          acc.v[q][j] += four;
-        }
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float four = xs[j][0] * __uint_as_float(wq[q].x);
+            four = fmaf(xs[j][1], __uint_as_float(wq[q].y), four);
+            four = fmaf(xs[j][2], __uint_as_float(wq[q].z), four);
+            four = fmaf(xs[j][3], __uint_as_float(wq[q].w), four);
+            acc.v[q][j0 + j] += four;
+          }
       }
     }
     st.issue(from);  // the stage's values have been used: it may be filled again
@@ -459,7 +476,7 @@ __device__ __forceinline__ void few_gate_up(FewStream<T>& st, uint32_t ring, int
   acc.clear();
   few_chunks<T, NT, false>(st, ring, slot, sg.left, x, 0, sg.chunk * (64 / (int)sizeof(T)), ntok,
                            [&](int j) { return (int64_t)tok[j] * d; }, acc, lane);
-  acc.store(red, lane);
+  acc.store(red, ntok, lane);
 }
 
 // Down of one group of 32 output columns: this warp's run over all entries, partial sums
