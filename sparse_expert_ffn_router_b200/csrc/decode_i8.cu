@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dec_stream_kernel(const __grid_
       int iter = 0;
       if (!ds_mma<kGateUp>(p, smem, c, S, 0, r, iter, tmem)) ds_abort(c, p.err);
       tc_commit(&c.drain);  // wait until every MMA issued by this thread has completed
-      mbar_wait_bounded(&c.drain, 0);
+      if (!mbar_wait_bounded(&c.drain, 0)) ds_abort(c, p.err);
     }
     __syncwarp();
   } else {
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(kD4Threads, 1) dec_stream4_kernel(const __grid
     if (lane == 0) {
       if (!d4_mma<kGateUp>(p, slots, ring, c, S, tmem)) ds_abort(c, p.err);
       tc_commit(&c.drain);
-      mbar_wait_bounded(&c.drain, 0);
+      if (!mbar_wait_bounded(&c.drain, 0)) ds_abort(c, p.err);
     }
     __syncwarp();
   } else if (warp < 6) {
@@ -1349,7 +1349,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dec_fused_kernel(const __grid_c
       if (ok) ok = ds_mma<false>(p.dn, smem, c, S, 1, r, iter, tmem);
       if (!ok) ds_abort(c, p.gu.err);
       tc_commit(&c.drain);
-      mbar_wait_bounded(&c.drain, 0);
+      if (!mbar_wait_bounded(&c.drain, 0)) ds_abort(c, p.gu.err);
     }
     __syncwarp();
   } else {

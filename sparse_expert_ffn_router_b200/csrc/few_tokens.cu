@@ -710,8 +710,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_tokens_kernel(const __grid
   }
   few_router(p, c);
   if (!few_barrier(p, c, 0)) {
-    few_barrier(p, c, 1);
-    if (p.d < kFewSplitRows * (int)gridDim.x) few_barrier(p, c, 2);
+    (void)few_barrier(p, c, 1);  // arrivals only: the counters stay in step
+    if (p.d < kFewSplitRows * (int)gridDim.x) (void)few_barrier(p, c, 2);
     return;
   }
   few_select(p, c, red);

@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
       if (lead) {
         if (!ok) raise_abort(m, err);
         tc_commit_pair(&m.drain);
-        mbar_wait_bounded(&m.drain, 0);
+        if (!mbar_wait_bounded(&m.drain, 0)) raise_abort(m, err);
       }
     }
     __syncwarp();
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid
     if (lead) {
       m.consumed = consumed;
       tc_commit(&m.tfull);  // also after an error: every MMA issued has ended
-      mbar_wait_bounded(&m.tfull, 0);
+      if (!mbar_wait_bounded(&m.tfull, 0)) raise_abort(m, err);  // no sums: nothing is exchanged or stored
     }
     __syncwarp();
   } else if (work && warp >= 2) {
@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid
   __syncthreads();  // this CTA's products have ended: its ring is idle
   if (threadIdx.x == 0 && m.abort)
     for (int i = m.consumed; i < m.issued; ++i)  // error path: copies that no product waited for
-      mbar_wait_bounded(&m.full[i % kSplitStages], (uint32_t)(i / kSplitStages) & 1u);
+      if (!mbar_wait_bounded(&m.full[i % kSplitStages], (uint32_t)(i / kSplitStages) & 1u)) break;
   __syncthreads();
   const bool ok = work && !m.abort;
   tc_fence_after();

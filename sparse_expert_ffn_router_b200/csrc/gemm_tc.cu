@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_ffn_kernel(const __grid_con
       m.consumed = consumed;
       // drain: wait until every MMA issued by this thread has completed
       tc_commit(&m.drain);
-      mbar_wait_bounded(&m.drain, 0);
+      if (!mbar_wait_bounded(&m.drain, 0)) raise_abort(m, p.err);
     }
     __syncwarp();
   } else {
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_ffn_kernel(const __grid_con
   if (threadIdx.x == 0 && m.abort) {
     // copies issued but never consumed: wait (bounded) until they land before exiting
     for (int i = m.consumed; i < m.issued; ++i)
-      mbar_wait_bounded(&m.full[i % STAGES], (uint32_t)(i / STAGES) & 1u);
+      if (!mbar_wait_bounded(&m.full[i % STAGES], (uint32_t)(i / STAGES) & 1u)) break;
   }
   __syncthreads();
   if (warp == 1) {
@@ -877,7 +877,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc2_ffn_kernel(const __grid_co
       }
       if (!ok) raise_abort(m, p.err);
       tc_commit_pair(&m.drain);
-      mbar_wait_bounded(&m.drain, 0);
+      if (!mbar_wait_bounded(&m.drain, 0)) raise_abort(m, p.err);
     }
     __syncwarp();
   } else {

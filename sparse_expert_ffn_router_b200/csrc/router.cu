@@ -310,6 +310,10 @@ __global__ void __launch_bounds__(kRtThreads, 1) router_tc_kernel(const __grid_c
   // ------------------------------------------------------------- epilogue
   const bool got = rt_wait(done, 0, abort_flag) && !*abort_flag;
   const bool warp_ok = __all_sync(0xffffffffu, got);
+  if (!warp_ok && lane == 0) {  // no logits: nothing is selected
+    *abort_flag = 1;
+    if (p.err) atomicOr(p.err, kErrWaitTimeout);
+  }
   tc_fence_after();
   const int q = warp & 3, half = warp >> 2;
   const int nchunks = p.N / 16, nc0 = (nchunks + 1) / 2;
@@ -456,7 +460,8 @@ __global__ void __launch_bounds__(kRtThreads, 1) router_tc_kernel(const __grid_c
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) {
     // copies issued but never consumed: wait (bounded) until they land before the CTA exits
-    for (int i = *consumed_s; i < *issued_s; ++i) mbar_wait_bounded(&full[i % S], (uint32_t)(i / S) & 1u);
+    for (int i = *consumed_s; i < *issued_s; ++i)
+      if (!mbar_wait_bounded(&full[i % S], (uint32_t)(i / S) & 1u)) break;
   }
   __syncthreads();
   if (warp == 0) {
