@@ -802,8 +802,23 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_ld_wait() {
+// The values pass through this after the wait, so that nothing computed from them can be scheduled before it.
+__device__ __forceinline__ void tmem_loaded(float (&v)[16]) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
+__device__ __forceinline__ void tmem_loaded(int (&v)[16]) {
+  asm volatile(""
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
+}
+// Waits for every load of this warp from TMEM; `v`: all values loaded since the last wait.
+template <typename... V>
+__device__ __forceinline__ void tmem_ld_wait(V&... v) {
+  static_assert(sizeof...(V) > 0, "name the values that are waited for");
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  (tmem_loaded(v), ...);
 }
 
 // ---------------------------------------------------------------------------------------

@@ -407,7 +407,7 @@ __device__ bool ds_epilogue(const DecStreamParams& p, DsCtl& c, int pre_idx, int
       if (p.nt8 == 8) {  // one load: columns 0-7 hi, 8-15 lo
         float v[16];
         tmem_ld16(tb, v);
-        tmem_ld_wait();
+        tmem_ld_wait(v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           hi[i] = (float)__float_as_int(v[i]);
@@ -417,7 +417,7 @@ __device__ bool ds_epilogue(const DecStreamParams& p, DsCtl& c, int pre_idx, int
         float vh[16], vl[16];
         tmem_ld16(tb + j, vh);
         tmem_ld16(tb + p.nt8 + j, vl);
-        tmem_ld_wait();
+        tmem_ld_wait(vh, vl);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           hi[i] = (float)__float_as_int(vh[i]);
@@ -764,7 +764,7 @@ __device__ __forceinline__ void d4_accumulate(float (&acc)[32], int nt8, int nto
   if (nt8 == 8) {
     float v[16];
     tmem_ld16(tb, v);
-    tmem_ld_wait();
+    tmem_ld_wait(v);
 #pragma unroll
     for (int t = 0; t < 8; ++t)
       acc[t] = fmaf(s, (float)__float_as_int(v[t]) + (float)__float_as_int(v[8 + t]) * (1.0f / 254.0f), acc[t]);
@@ -775,7 +775,7 @@ __device__ __forceinline__ void d4_accumulate(float (&acc)[32], int nt8, int nto
       float vh[16], vl[16];
       tmem_ld16(tb + j, vh);
       tmem_ld16(tb + nt8 + j, vl);
-      tmem_ld_wait();
+      tmem_ld_wait(vh, vl);
 #pragma unroll
       for (int t = 0; t < 16; ++t)
         acc[j + t] = fmaf(s, (float)__float_as_int(vh[t]) + (float)__float_as_int(vl[t]) * (1.0f / 254.0f), acc[j + t]);

@@ -279,16 +279,6 @@ __device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __float_as_int(f[i]);
 }
 
-// Waits for the loads of this warp from TMEM; the values pass through it, so that nothing computed from
-// them can be scheduled before it.
-__device__ __forceinline__ void tmem_ld_wait16(int (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
-               : "memory");
-}
-
 // Two fp32 values per instruction: the epilogue is bound by the instructions it issues.
 struct Pair {
   unsigned long long v;
@@ -634,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
           for (int c = 16 * half; c < trows; c += 16 * kEpiHalves) {
             int v[16];
             tmem_ld16i(tb + c, v);
-            tmem_ld_wait();
+            tmem_ld_wait(v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float x = c + i < trows ? (float)v[i] * (rs[(c + i) & (kLightRows - 1)] * tn) : 0.f;
@@ -649,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
           for (int c = 16 * half; c < trows; c += 16 * kEpiHalves) {
             int v[16];
             tmem_ld16i(tb + c, v);
-            tmem_ld_wait();
+            tmem_ld_wait(v);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (c + i < trows && oc < p.N)
@@ -692,8 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
           for (int b = 0; b < kBlocks; ++b) {
             const int c = c0 + 16 * b;
             if (c < ncols) {
-              tmem_ld_wait16(g[b & 1]);
-              if (kSwiglu) tmem_ld_wait16(u[b & 1]);
+              if (kSwiglu) tmem_ld_wait(g[b & 1], u[b & 1]);
+              else tmem_ld_wait(g[b & 1]);
               if (b + 1 < kBlocks && c + 16 < ncols) load(c + 16, g[(b + 1) & 1], u[(b + 1) & 1]);
               finish(c, g[b & 1], u[b & 1]);
             }
@@ -904,7 +894,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid
           for (int c = 0; c < own; c += 16) {
             int v[16];
             tmem_ld16i(tb + part * kCols + to * own + c, v);
-            tmem_ld_wait16(v);
+            tmem_ld_wait(v);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int unit = rank * units + (part * own + c) / 4 + i;
@@ -924,7 +914,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid
     constexpr int kBlock = kOutRow / (int)sizeof(Out);  // columns of a gathered block
     auto sums = [&](int part, int c, int (&v)[16]) {
       tmem_ld16i(tb + part * kCols + c_first + c, v);
-      tmem_ld_wait16(v);
+      tmem_ld_wait(v);
       for (int j = 1; j < S; ++j) {
         const int from = (rank + j) % S;
 #pragma unroll

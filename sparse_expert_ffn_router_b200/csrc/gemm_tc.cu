@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_ffn_kernel(const __grid_con
           float v0[16], v1[16];
           tmem_ld16(tb + j0, v0);
           tmem_ld16(tb + 128 + j0, v1);
-          tmem_ld_wait();
+          tmem_ld_wait(v0, v1);
           if (kGateUp) {
             if (t.n0 + ch < n_out) {
 #pragma unroll
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_ffn_kernel(const __grid_con
           float g[16], u[16];
           tmem_ld16(tb + c, g);
           tmem_ld16(tb + BN / 2 + c, u);
-          tmem_ld_wait();
+          tmem_ld_wait(g, u);
           if (valid && t.n0 + c < n_out) {
             uint32_t pk[8];
 #pragma unroll
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc_ffn_kernel(const __grid_con
         for (int c = 0; c < BN; c += 16) {
           float v[16];
           tmem_ld16(tb + c, v);
-          tmem_ld_wait();
+          tmem_ld_wait(v);
           if (valid && t.n0 + c < n_out) {
             uint32_t pk[8];
 #pragma unroll
@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc2_ffn_kernel(const __grid_co
           for (int c = 0; c < trows; c += 16) {
             float v[16];
             tmem_ld16(tb + c, v);
-            tmem_ld_wait();
+            tmem_ld_wait(v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float up = __shfl_down_sync(0xffffffffu, v[i], 16);
@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc2_ffn_kernel(const __grid_co
           for (int c = 0; c < trows; c += 16) {
             float v[16];
             tmem_ld16(tb + c, v);
-            tmem_ld_wait();
+            tmem_ld_wait(v);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (c + i < trows && oc < n_out) out[(size_t)(t.row0 + c + i) * n_out + oc] = __float2bfloat16_rn(v[i]);
@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc2_ffn_kernel(const __grid_co
           float g[16], u[16];
           tmem_ld16(tb + c, g);
           tmem_ld16(tb + BN / 2 + c, u);
-          tmem_ld_wait();
+          tmem_ld_wait(g, u);
           if (valid && t.n0 + c < n_out) {
             uint32_t pk[8];
 #pragma unroll
@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) tc2_ffn_kernel(const __grid_co
         for (int c = 0; c < BN; c += 16) {
           float v[16];
           tmem_ld16(tb + c, v);
-          tmem_ld_wait();
+          tmem_ld_wait(v);
           if (valid && t.n0 + c < n_out) {
             uint32_t pk[8];
 #pragma unroll

@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) router_tc_kernel(const __grid_c
       for (int c = cbeg; c < cend; ++c) {
         float v[16];
         tmem_ld16(tbase + c * 16, v);
-        tmem_ld_wait();
+        tmem_ld_wait(v);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (c * 16 + i < p.E) offer(i % kChains, c * 16 + i, v[i]);
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) router_tc_kernel(const __grid_c
       for (int c = cbeg; c < cend; ++c) {
         float v[16];
         tmem_ld16(tbase + c * 16, v);
-        tmem_ld_wait();
+        tmem_ld_wait(v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) st_shared_cluster_f32(dst + (uint32_t)((c * 16 + i) * tpc) * 4u, v[i]);
       }

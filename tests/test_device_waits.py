@@ -1,4 +1,5 @@
-"""Reads the CUDA sources: every bounded wait's outcome is looked at.
+"""Reads the CUDA sources: every bounded wait's outcome is looked at, and every read of the tensor cores'
+accumulators waits for the values it names.
 
 A wait on the device gives up after a time limit.  The only report that a user gets of it is the error
 word that the caller of the wait sets, so a call whose result is dropped would let a kernel store what
@@ -45,3 +46,12 @@ def test_the_reading_finds_dropped_results():
 @pytest.mark.parametrize("name", sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu*"))))
 def test_no_wait_result_is_dropped(name):
     assert dropped(_code(os.path.join(CSRC, name))) == []
+
+
+@pytest.mark.parametrize("name", sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu*"))))
+def test_loads_from_tensor_memory_pass_through_their_wait(name):
+    # tcgen05.ld delivers its registers later; arithmetic on them is held behind the wait only if the wait
+    # has them as operands (a clobber of memory does not order arithmetic)
+    src = _code(os.path.join(CSRC, name))
+    assert not re.search(r"tmem_ld_wait\w*\(\s*\)\s*;", src)
+    assert src.count("tcgen05.wait::ld") == (1 if name == "common.cuh" else 0)
