@@ -282,7 +282,8 @@ colibri_status colibri_quantize_rows(const void* x, int32_t act_dtype, int32_t r
 
 /*
  * colibri_int_gemm -- y[m][n] = a_scale[m] * w_scale[n] * sum_k A[m][k] * W[n][k] for A [M, K],
- * W [N, K] (rows = output channels), y [M, N] in out_dtype (F32 or BF16).
+ * W [N, K] (rows = output channels), y [M, N] in out_dtype (F32 or BF16).  The value counts, not
+ * the order of the products: a_scale * w_scale alone may be too small or too large for fp32.
  */
 colibri_status colibri_int_gemm(const int8_t* A, int64_t lda, const float* a_scale,
                                 const int8_t* W, int64_t ldw, const float* w_scale, int32_t M,

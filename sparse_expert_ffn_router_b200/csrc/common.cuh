@@ -429,6 +429,19 @@ cudaError_t configure_int_kernels();  // once per device, before any launch insi
 // ---------------------------------------------------------------------------------------
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
+// Scales of the int8 products, y = acc * s * t.  Between 2^-63 and 2^63 the product of any two scales is a
+// normal number, so (float)acc * (s * t) rounds three times and that is all; outside of it s * t may lose
+// bits or overflow where the result does not (quantised rows have scales down to 2^-126), and the product
+// is formed in 64 bits.  Zero and NaN give what they should either way.
+__device__ __forceinline__ bool scale_wide(float s) {  // without branches: loads of scales stay ahead of it
+  const uint32_t a = __float_as_uint(s) & 0x7fffffffu;
+  return (a - 0x20000000u > 0x5f000000u - 0x20000000u) & (a != 0u);  // 2^-63, 2^63
+}
+__device__ __forceinline__ float scaled(int acc, float s, float t) {
+  if (scale_wide(s) | scale_wide(t)) return (float)((double)acc * (double)s * (double)t);
+  return (float)acc * (s * t);
+}
+
 // Two int8 planes of a value, given the row scale a and 1/a: hi = rint(x / a), lo = rint((x - a hi)
 // * 254 / a), both clamped to [-127, 127], so that x ~= a * (hi + lo / 254).
 __device__ __forceinline__ void split_planes(float x, float a, float inv_a, int& qh, int& ql) {

@@ -5,7 +5,8 @@
 //
 // The rows may be grouped: rows [offsets[e], offsets[e+1]) meet the weights of expert e.  The sums
 // over k are exact int32 (K <= 131056, so that K * 128 * 128 stays below 2^31); the conversion to
-// fp32 and the two scales round once each, and the result once to its type.
+// fp32 and the two scales round once each (with a scale outside 2^-63..2^63 once in all, from 64 bits),
+// and the result once to its type.
 //
 // i8_pair_kernel: clusters of two CTAs (tcgen05 cta_group::2, kind::i8), persistent, one pair per two
 // SMs, 352 threads per CTA:
@@ -116,6 +117,7 @@ struct PairSmem {
   Tile tile[kPlans];
   alignas(16) float col[kPlans][kBN];  // column scales of the tile (SwiGLU: gate | up)
   alignas(16) float row[kPlans][128];  // row scales: of this CTA's rows, or of a swapped tile's
+  int wide[kPlans];                    // some scale is wide (the others' tiles are spared the question per value)
   alignas(16) uint8_t out[kEpiWarps][32 * kOutPitch];
 };
 constexpr size_t kPairTok = (size_t)kStages * 2 * kTok;
@@ -370,6 +372,46 @@ __device__ __forceinline__ void store_block(Out* dst, int64_t ldy, const uint8_t
   __syncwarp();
 }
 
+// The epilogue of a tile with a wide scale, apart from the others': value by value, a lane per row, or in a swapped
+// tile per column.
+template <bool kSwiglu, typename Out>
+__device__ __noinline__ void wide_tile(const PairParams& p, PairSmem& m, int slot, uint32_t tb, int rank, int q, int half,
+                                       int lane) {
+  const Tile t = m.tile[slot];
+  const int trows = t.row_end - t.row0;
+  const float *col = m.col[slot], *rs = m.row[slot];
+  Out* const y = static_cast<Out*>(p.y);
+  constexpr int kCols = kSwiglu ? kBN / 2 : kBN;
+  const bool light = trows <= p.light_rows;
+  // the accumulator's column c and lane are row c and column `oc` of a swapped tile, column c and row `row` of
+  // a full one
+  const int c0 = kSwiglu ? 64 * rank + 16 * q + (lane & 15) : 128 * rank + 32 * q + lane;
+  const int oc = t.n0 + c0, row = 128 * rank + 32 * q + lane;
+  const int n = light ? trows : (128 * rank + 32 * q < trows ? min(kCols, p.N - t.n0) : 0);
+  const bool gate = !kSwiglu || lane < 16;
+  for (int c = 16 * half; c < n; c += 16 * kEpiHalves) {
+    int v[16], u[16];
+    tmem_ld16i(tb + c, v);
+    tmem_ld16i(tb + (kSwiglu && !light ? kBN / 2 : 0) + c, u);
+    tmem_ld_wait(v, u);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x;
+      if (light) {
+        const float tn = col[(gate ? 0 : kBN / 2) + c0];
+        x = c + i < trows ? scaled(v[i], rs[c + i], tn) : 0.f;
+        if (kSwiglu) x = silu_mul_fast(x, __shfl_down_sync(0xffffffffu, x, 16));
+        if (gate && c + i < trows && oc < p.N) y[(int64_t)(t.row0 + c + i) * p.ldy + oc] = from_f32<Out>(x);
+      } else {
+        const float sr = rs[32 * q + lane];
+        x = scaled(v[i], sr, col[c + i]);
+        if (kSwiglu) x = silu_mul_fast(x, scaled(u[i], sr, col[kBN / 2 + c + i]));
+        if (row < trows && c + i < n) y[(int64_t)(t.row0 + row) * p.ldy + t.n0 + c + i] = from_f32<Out>(x);
+      }
+    }
+  }
+}
+
 template <bool kSwiglu, typename Out>
 __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -586,10 +628,19 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
       const int r0 = trows <= p.light_rows ? t.row0 : t.row0 + 128 * (int)rank;
 #pragma unroll
       for (int i = 0; i < 4; ++i) rs[i] = r0 + lane + 32 * i < t.row_end ? __ldg(p.a_scale + r0 + lane + 32 * i) : 0.f;
+      bool wide = false;
 #pragma unroll
-      for (int i = 0; i < kBN / 32; ++i) m.col[slot][lane + 32 * i] = cs[i];
+      for (int i = 0; i < kBN / 32; ++i) {
+        m.col[slot][lane + 32 * i] = cs[i];
+        wide |= scale_wide(cs[i]);
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m.row[slot][lane + 32 * i] = rs[i];
+      for (int i = 0; i < 4; ++i) {
+        m.row[slot][lane + 32 * i] = rs[i];
+        wide |= scale_wide(rs[i]);
+      }
+      wide = __any_sync(0xffffffffu, wide);
+      if (lane == 0) m.wide[slot] = wide;
       __syncwarp();
       if (lane == 0) mbar_arrive(&m.sfull[slot]);
     }
@@ -614,7 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) i8_pair_kernel(const __grid_const
       const bool light = trows <= p.light_rows;
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * kBN);
       const float* col = m.col[slot];
-      if (light) {
+      if (m.wide[slot]) {
+        wide_tile<kSwiglu, Out>(p, m, slot, tb, (int)rank, q, half, lane);
+      } else if (light) {
         // TMEM lane = weight row of this CTA, column c = the tile's row t.row0 + c
         const float* rs = m.row[slot];
         if (kSwiglu) {
@@ -744,6 +797,7 @@ struct SplitSmem {
   uint32_t tmem_base;
   int abort;
   int issued, consumed;
+  int wide;  // some scale of the tile is wide
   int32_t off[kMaxExperts + 1];
   int32_t mt[kMaxExperts + 1];
   alignas(16) float col[kSplitTile];
@@ -778,7 +832,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid
     }
     mbar_init(&m.tfull, 1);
     m.abort = 0;
-    m.issued = m.consumed = 0;
+    m.issued = m.consumed = m.wide = 0;
     mbar_fence_init();
     tma_prefetch_desc(&p.mapA);
     tma_prefetch_desc(&p.mapB);
@@ -869,6 +923,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid
     const int n = t.n0 + (kSwiglu ? i & (kCols - 1) : i);
     m.col[i] = n < p.N ? __ldg(ws + (kSwiglu && i >= kCols ? p.N : 0) + n) : 0.f;
     m.row[i] = t.row0 + i < t.row_end ? __ldg(p.a_scale + t.row0 + i) : 0.f;
+    if (scale_wide(m.col[i]) || scale_wide(m.row[i])) m.wide = 1;
   }
   __syncthreads();  // this CTA's products have ended: its ring is idle
   if (threadIdx.x == 0 && m.abort)
@@ -933,10 +988,18 @@ __global__ void __launch_bounds__(kSplitThreads, 1) i8_split_kernel(const __grid
       sums(0, c, g);
       if (kSwiglu) sums(1, c, u);
       float v[16];
+      if (m.wide) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        v[i] = (float)g[i] * (sr * m.col[c_first + c + i]);
-        if (kSwiglu) v[i] = silu_mul_fast(v[i], (float)u[i] * (sr * m.col[kCols + c_first + c + i]));
+        for (int i = 0; i < 16; ++i) {
+          v[i] = scaled(g[i], sr, m.col[c_first + c + i]);
+          if (kSwiglu) v[i] = silu_mul_fast(v[i], scaled(u[i], sr, m.col[kCols + c_first + c + i]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          v[i] = (float)g[i] * (sr * m.col[c_first + c + i]);
+          if (kSwiglu) v[i] = silu_mul_fast(v[i], (float)u[i] * (sr * m.col[kCols + c_first + c + i]));
+        }
       }
       gather16<Out>(m.out[q], lane, c * (int)sizeof(Out) & (kOutRow - 1), v);
       const int at = c & ~(kBlock - 1);  // the block's first column

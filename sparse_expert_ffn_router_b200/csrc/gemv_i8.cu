@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) i8_skinny_kernel(const SkinnyPara
         if (max(from, i * chunks) < min(to, (i + 1) * chunks)) s += red[(i + w) * kSlot + lane * kPitch + warp];
         from = to;
       }
-      y[warp * p.ldy + n] = from_f32<Out>((float)s * (__ldg(p.a_scale + warp) * __ldg(p.w_scale + n)));
+      y[warp * p.ldy + n] = from_f32<Out>(scaled(s, __ldg(p.a_scale + warp), __ldg(p.w_scale + n)));
     }
     __syncthreads();
   }
