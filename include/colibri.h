@@ -107,7 +107,8 @@ typedef enum {
  *                   logits renormalised over the k chosen.  Selection (logit descending, lower
  *                   expert index on ties) is the same for every variant, applied to the clamped
  *                   logits when COLIBRI_ROUTER_CLAMP is set (logits above 50 then tie and go to
- *                   the lower index).  Unknown bits: COLIBRI_ERR_INVALID_ARG.
+ *                   the lower index).  A logit that is NaN is not chosen while there are k numbers
+ *                   (the clamp makes -50 of it).  Unknown bits: COLIBRI_ERR_INVALID_ARG.
  *   weight_scale_mode  COLIBRI_I8 weights: COLIBRI_SCALE_PER_CHANNEL (0) or
  *                   COLIBRI_SCALE_PER_MATRIX; must be 0 for other weight types (INVALID_ARG).
  *                   W[o][i] = s * q[o][i] with s the channel's or the matrix's scale.

@@ -556,9 +556,11 @@ __device__ __forceinline__ void few_router(const FewParams<T>& p, FewCtl& c) {
 
 // One warp selects the top-k of one token from its E logits in shared memory: the largest value first,
 // lower index on ties.  The values are compared as integers in their order (adding zero makes -0 and 0
-// the same value), so that a step is two warp reductions; the experts chosen are distinct whatever the
-// values are.
+// the same value), so that a step is two warp reductions.  A NaN comes after every number and weighs
+// nothing beside one (the layer's other selections never take it); it is asked for by itself, since its bits
+// after an addition are the compiler's choice.  The experts chosen are distinct whatever the values are.
 __device__ __forceinline__ void few_topk(const float* lg, int E, int k, int flags, int lane, int32_t* idx, float* w) {
+  constexpr uint32_t kNan = 1u;  // below the key of -infinity
   uint32_t key[kMaxExperts / 32];
 #pragma unroll
   for (int m = 0; m < kMaxExperts / 32; ++m) {
@@ -566,7 +568,7 @@ __device__ __forceinline__ void few_topk(const float* lg, int E, int k, int flag
     key[m] = 0u;  // no such expert, or chosen already
     if (e < E) {
       const uint32_t b = __float_as_uint(router_clamp(lg[e], flags) + 0.f);
-      key[m] = max(1u, b & 0x80000000u ? ~b : b | 0x80000000u);
+      key[m] = (b & 0x7fffffffu) > 0x7f800000u ? kNan : b & 0x80000000u ? ~b : b | 0x80000000u;
     }
   }
   float den = 0.f, first = 0.f, mine = 0.f;
@@ -586,7 +588,7 @@ __device__ __forceinline__ void few_topk(const float* lg, int E, int k, int flag
 #pragma unroll
     for (int m = 0; m < kMaxExperts / 32; ++m)
       if (e == lane + 32 * m) key[m] = 0u;
-    const float v = __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
+    const float v = top == kNan ? -INFINITY : __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
     if (j == 0) first = v;
     const float p = (flags & kRouterRaw) ? v : expf(v - first);
     den += p;
