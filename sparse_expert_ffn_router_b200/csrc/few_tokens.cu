@@ -279,20 +279,28 @@ struct FewStream {
   }
 };
 
-// Sums of one lane over chunks: bf16 [2 blocks of 16 weight rows][NT blocks of 8 columns][4], in the
-// instruction's layout; fp32 [4 rows][8 NT columns], this lane's part of each chunk.
-template <typename T, int NT>
+// Sums of one lane over chunks: bf16 [P parts of the columns' values][2 blocks of 16 weight rows][NT blocks
+// of 8 columns][4], in the instruction's layout; fp32 [4 rows][8 NT columns], this lane's part of each chunk.
+// The sum over the second part of H stands apart, because it counts only beside a finite sum over the
+// first: where that is infinite (a weight or H is), this one is infinite of either sign or NaN.
+template <typename T, int NT, int P>
 struct FewAcc;
-template <int NT>
-struct FewAcc<__nv_bfloat16, NT> {
-  float v[2][NT][4];
+template <int NT, int P>
+struct FewAcc<__nv_bfloat16, NT, P> {
+  float v[P][2][NT][4];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int h = 0; h < P; ++h)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[m][j][i] = 0.f;
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[h][m][j][i] = 0.f;
+  }
+  __device__ __forceinline__ float sum(int m, int j, int i) const {
+    const float hi = v[0][m][j][i];
+    return P == 2 && fabsf(hi) < INFINITY ? hi + v[P - 1][m][j][i] : hi;
   }
   // row q * 8 + g of the tile, token columns 8 j + 2 t and the next
   __device__ __forceinline__ void store(float* red, int, int lane) {
@@ -304,7 +312,7 @@ struct FewAcc<__nv_bfloat16, NT> {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           *reinterpret_cast<float2*>(red + ((2 * m + i) * 8 + g) * kFewPitch + 8 * j + 2 * t) =
-              make_float2(v[m][j][2 * i], v[m][j][2 * i + 1]);
+              make_float2(sum(m, j, 2 * i), sum(m, j, 2 * i + 1));
   }
   // the sums of column j, times its weight, onto column tok[j] of red
   __device__ __forceinline__ void add(float* red, const uint8_t* tok, const float* w, int n, int lane) {
@@ -320,14 +328,14 @@ struct FewAcc<__nv_bfloat16, NT> {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float* d = red + (q * 8 + g) * kFewPitch + to;
-            *d = fmaf(wt, v[q >> 1][j][2 * (q & 1) + b], *d);
+            *d = fmaf(wt, sum(q >> 1, j, 2 * (q & 1) + b), *d);
           }
         }
       }
   }
 };
-template <int NT>
-struct FewAcc<float, NT> {
+template <int NT, int P>
+struct FewAcc<float, NT, P> {
   float v[4][8 * NT];
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -374,10 +382,9 @@ struct FewAcc<float, NT> {
 // `n` chunks of the stream times the rows of `ncol` columns; column j has its row at row(j) elements
 // behind `rows`; `at`: the first chunk's element.  kH: the rows were written by this launch (read them
 // from L2; bf16: their second part lies `lo` elements behind the first).
-template <typename T, int NT, bool kH, typename Row>
+template <typename T, int NT, bool kH, int P, typename Row>
 __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int& slot, int n, const T* rows, int64_t lo,
-                                           int at, int ncol, Row row, FewAcc<T, NT>& acc, int lane) {
-  constexpr int P = kH && sizeof(T) == 2 ? 2 : 1;
+                                           int at, int ncol, Row row, FewAcc<T, NT, P>& acc, int lane) {
   const int g = lane >> 2, t = lane & 3;
   constexpr int CE = 64 / sizeof(T);
   // volatile: the compiler would move the loads for the next chunk behind the wait for this one
@@ -431,8 +438,8 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             const uint4& x = xb[h][j];
-            mma_bf16(acc.v[m][j], wq[2 * m].x, wq[2 * m + 1].x, wq[2 * m].y, wq[2 * m + 1].y, x.x, x.y);
-            mma_bf16(acc.v[m][j], wq[2 * m].z, wq[2 * m + 1].z, wq[2 * m].w, wq[2 * m + 1].w, x.z, x.w);
+            mma_bf16(acc.v[h][m][j], wq[2 * m].x, wq[2 * m + 1].x, wq[2 * m].y, wq[2 * m + 1].y, x.x, x.y);
+            mma_bf16(acc.v[h][m][j], wq[2 * m].z, wq[2 * m + 1].z, wq[2 * m].w, wq[2 * m + 1].w, x.z, x.w);
           }
     } else {
       // every lane needs every column's bytes: they come from the lane that loaded them, J columns at a
@@ -472,7 +479,7 @@ __device__ __forceinline__ void few_chunks(FewStream<T>& st, uint32_t ring, int&
 template <typename T, int NT>
 __device__ __forceinline__ void few_gate_up(FewStream<T>& st, uint32_t ring, int& slot, const FewSeg& sg, const T* x,
                                             int d, const uint8_t* tok, int ntok, float* red, int lane) {
-  FewAcc<T, NT> acc;
+  FewAcc<T, NT, 1> acc;
   acc.clear();
   few_chunks<T, NT, false>(st, ring, slot, sg.left, x, 0, sg.chunk * (64 / (int)sizeof(T)), ntok,
                            [&](int j) { return (int64_t)tok[j] * d; }, acc, lane);
@@ -485,7 +492,7 @@ template <typename T, int NT>
 __device__ __forceinline__ void few_down_segment(FewStream<T>& st, uint32_t ring, int& slot, const FewSeg& sg, const T* H,
                                                  int64_t lo, int f, const uint8_t* tok, const float* w, int ntok,
                                                  float* red, int lane) {
-  FewAcc<T, NT> acc;
+  FewAcc<T, NT, sizeof(T) == 2 ? 2 : 1> acc;
   acc.clear();
   few_chunks<T, NT, true>(st, ring, slot, sg.left, H, lo, sg.chunk * (64 / (int)sizeof(T)), ntok,
                           [&](int j) { return (int64_t)j * f; }, acc, lane);

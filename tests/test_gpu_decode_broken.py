@@ -70,3 +70,50 @@ def test_fewer_numbers_than_choices(dt):
     c.rb = torch.full((4,), NAN, device="cuda")
     y, f, a, b = _both(c)
     assert torch.isnan(y).all() and torch.isnan(f).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("T,d,f,fs", [(2, 64, 64, 0), (12, 256, 320, 64), (16, 4096, 192, 0)])
+def test_infinite_down_weights(T, d, f, fs, dt):
+    """One infinite value in W2: the output it belongs to is an infinity of its and h's sign in every token,
+    as the product with h itself gives, and the other outputs stay as they were."""
+    c = Case(T, d, f, 3, 2, fs, dt)
+    c.rb = torch.tensor([9.0, 0.0, 0.0], device="cuda")  # every token chooses expert 0
+    clean = c.decode().clone()
+    x = c.x.double()
+    w1, w3 = (c.ew[0, i * f * d: (i + 1) * f * d].view(f, d).double() for i in (0, 1))
+    g = x @ w1.T
+    h = g * torch.sigmoid(g) * (x @ w3.T)
+    col = int(h.abs().amin(0).argmax())          # h of this column is clear of zero in every token
+    assert float(h[:, col].abs().min()) > 1e-4
+    w2 = c.ew[0, 2 * f * d: 3 * f * d].view(d, f)
+    rows = [0, 5, d - 1]
+    for i, o in enumerate(rows):
+        w2[o, col] = INF if i % 2 == 0 else -INF
+    y, fwd, _, _ = _both(c)
+    for i, o in enumerate(rows):
+        want = torch.sign(h[:, col]) * (INF if i % 2 == 0 else -INF)
+        assert torch.equal(y[:, o].double(), want) and torch.equal(fwd[:, o].double(), want)
+    keep = [o for o in range(d) if o not in rows]
+    assert torch.equal(y[:, keep], clean[:, keep])
+
+
+@pytest.mark.gpu
+def test_infinite_down_weights_beside_a_short_h():
+    # h is a bf16 number as it is, or just above or below one: nothing, or something of either sign, is left of it
+    c = Case(3, 64, 64, 1, 1, 0, BF16)
+    f, d = c.f, c.d
+    c.x.zero_()
+    c.x[:, 0] = torch.tensor([1.0, 1.0, 1.0])
+    c.ew.zero_()
+    c.ew[0, 0] = 64.0                                          # g = 64, silu(g) = 64
+    c.ew[0, f * d] = 1.0                                       # u = 1 (+ small parts of x[1], x[2])
+    c.ew[0, f * d + 1] = 2.0 ** -10
+    c.ew[0, f * d + 2] = -2.0 ** -10
+    c.x[1, 1] = 1.0
+    c.x[2, 2] = 1.0
+    c.ew[0, 2 * f * d: 3 * f * d].view(d, f)[:, 0] = INF       # h = 64, 64 (1 + 2^-10), 64 (1 - 2^-10)
+    y = c.decode()
+    torch.cuda.synchronize()
+    assert (y == INF).all()
