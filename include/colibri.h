@@ -322,10 +322,18 @@ colibri_status colibri_int_swiglu_experts(const int8_t* A, int64_t lda, const fl
 /*
  * colibri_int_check -- synchronise `stream` and report whether a bounded device wait of an int8
  * product called since the last check on the current device gave up (COLIBRI_ERR_TIMEOUT; that
- * product's output is then undefined).  One word per device, shared by all streams, cleared by the
- * check.  Blocking.  Errors: TIMEOUT, CUDA.
+ * product's output is then undefined).  One word per device, shared by all streams: a check
+ * reports what any stream's products have left there by then, and clears it in the same step, so
+ * that nothing is lost and nothing reported twice.  Blocking.  Errors: TIMEOUT, CUDA.
  */
 colibri_status colibri_int_check(void* stream);
+
+/*
+ * colibri_int_selftest_wait_timeout -- colibri_selftest_wait_timeout for the int8 products: a wait
+ * on the current device that runs out after `timeout_us` microseconds (1..1000000) and is reported
+ * by the next colibri_int_check.  Errors: INVALID_ARG, CUDA.
+ */
+colibri_status colibri_int_selftest_wait_timeout(int32_t timeout_us, void* stream);
 
 /*
  * colibri_sync_status -- synchronise `stream`, then read and clear the context's device

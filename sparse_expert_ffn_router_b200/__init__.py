@@ -44,6 +44,7 @@ EXPORTS = (
     "colibri_int_gemm_experts",
     "colibri_int_swiglu_experts",
     "colibri_int_check",
+    "colibri_int_selftest_wait_timeout",
     "colibri_sync_status",
     "colibri_profile_begin",
     "colibri_profile_end",
@@ -115,6 +116,8 @@ def load() -> ctypes.CDLL:
         f.restype = ctypes.c_int
     lib.colibri_int_check.argtypes = [vp]
     lib.colibri_int_check.restype = ctypes.c_int
+    lib.colibri_int_selftest_wait_timeout.argtypes = [i32, vp]
+    lib.colibri_int_selftest_wait_timeout.restype = ctypes.c_int
     lib.colibri_sync_status.argtypes = [vp, vp]
     lib.colibri_sync_status.restype = ctypes.c_int
     lib.colibri_profile_begin.argtypes = [vp, i32]
@@ -250,6 +253,11 @@ def colibri_int_swiglu_experts(A, lda: int, a_scale, rows: int, offsets, num_exp
 def colibri_int_check(stream=None) -> None:
     """Raises ColibriError(TIMEOUT) if a device wait of an int8 product gave up since the last check."""
     _check(load().colibri_int_check(_stream(stream)), "colibri_int_check")
+
+
+def colibri_int_selftest_wait_timeout(timeout_us: int, stream=None) -> None:
+    """A device wait that runs out, reported by the next colibri_int_check (see include/colibri.h)."""
+    _check(load().colibri_int_selftest_wait_timeout(timeout_us, _stream(stream)), "colibri_int_selftest_wait_timeout")
 
 
 def colibri_sync_status(ctx: int, stream=None) -> None:

@@ -417,7 +417,8 @@ struct IntGemmArgs {
 };
 constexpr int kSkinnyRows = 16;  // one group of at most this many rows: gemv_i8.cu
 cudaError_t launch_int_skinny(const IntGemmArgs& a, int sms, cudaStream_t s);
-cudaError_t int_gemm_take_error(uint32_t* word);  // reads and clears the current device's own word
+cudaError_t int_gemm_error_word(uint32_t** word);  // the current device's own word
+cudaError_t int_gemm_take_error(uint32_t* word, cudaStream_t s);  // reads and clears it; waits for `s`
 cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s);
 // dst: nullptr, or [rows, k]: row r's integers and scale go to rows dst[r][0..k) instead of to row r
 cudaError_t launch_quantize_rows(const void* x, int act, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,

@@ -49,6 +49,7 @@
 //
 // Every wait is bounded (kWaitTimeoutNs); one that gives up sets the error word and ends all roles.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "common.cuh"
@@ -58,6 +59,16 @@ namespace {
 
 // Set by a bounded wait that gave up, when the caller brings no word of its own.
 __device__ uint32_t g_int_err;
+// What a check found there on its way to the host: a word per check, in turn, since checks may run at once.
+constexpr unsigned kTaken = 256;
+__device__ uint32_t g_int_taken[kTaken];
+
+// Reads and clears the error word in one step: a wait that gives up meanwhile stays for the next check.
+__global__ void take_error_kernel(unsigned slot) {
+  pdl_trigger();
+  pdl_wait();
+  g_int_taken[slot] = atomicExch(&g_int_err, 0u);
+}
 
 constexpr int kEpiWarps = 8;          // two per quarter of the TMEM lanes (one: fine-grained down 96 against 92 us)
 constexpr int kEpiHalves = kEpiWarps / 4;
@@ -1151,12 +1162,19 @@ cudaError_t configure_int_kernels() {
   return e;
 }
 
-// The error word of calls without one of their own, read and cleared (after `s` is idle).
-cudaError_t int_gemm_take_error(uint32_t* word) {
-  cudaError_t e = cudaMemcpyFromSymbol(word, g_int_err, sizeof(uint32_t));
-  const uint32_t zero = 0;
-  if (e == cudaSuccess && *word) e = cudaMemcpyToSymbol(g_int_err, &zero, sizeof(zero));
-  return e;
+cudaError_t int_gemm_error_word(uint32_t** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_int_err);
+}
+
+// The error word of calls without one of their own, read and cleared behind the work on `s`.
+cudaError_t int_gemm_take_error(uint32_t* word, cudaStream_t s) {
+  static std::atomic<unsigned> next{0};
+  const unsigned slot = next.fetch_add(1u) % kTaken;
+  cudaError_t e = launch_kernel(take_error_kernel, dim3(1), dim3(1), 0, s, 1, slot);
+  if (e == cudaSuccess)
+    e = cudaMemcpyFromSymbolAsync(word, g_int_taken, sizeof(uint32_t), slot * sizeof(uint32_t), cudaMemcpyDeviceToHost, s);
+  const cudaError_t done = cudaStreamSynchronize(s);
+  return e != cudaSuccess ? e : done;
 }
 
 }  // namespace colibri

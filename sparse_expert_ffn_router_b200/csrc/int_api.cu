@@ -157,7 +157,7 @@ colibri_status colibri_int_check(void* stream) {
     return refuse(COLIBRI_ERR_CUDA, "stream synchronize failed");
   }
   uint32_t word = 0;
-  const cudaError_t e = int_gemm_take_error(&word);
+  const cudaError_t e = int_gemm_take_error(&word, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return launched(e, "reading the error word");
   if (word) return refuse(COLIBRI_ERR_TIMEOUT, "a bounded device wait of an int8 product gave up");
   return COLIBRI_OK;
