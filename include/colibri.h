@@ -217,7 +217,8 @@ colibri_status colibri_moe_forward_routed(colibri_ctx* ctx, const void* x, int32
  * within the rounding of their sums, not bit for bit; a call's result does not vary from run to
  * run.  The launch needs every SM of the device for a CTA of 512 threads: beside other work it
  * starts once they are free.  Errors: INVALID_ARG (also T > 16), ALIGNMENT, UNSUPPORTED
- * (quantised weights, which colibri_moe_forward streams at these sizes), CUDA.
+ * (quantised weights: colibri_moe_forward runs those layers, with COLIBRI_I8 weights as one launch,
+ * with the other types as several), CUDA.
  */
 colibri_status colibri_moe_decode(colibri_ctx* ctx, const void* x, int32_t T,
                                   const void* router_w, const float* router_b,

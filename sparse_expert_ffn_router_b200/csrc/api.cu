@@ -903,7 +903,7 @@ colibri_status colibri_moe_decode(colibri_ctx* ctx, const void* x, int32_t T, co
   if (!ctx) return fail(nullptr, COLIBRI_ERR_INVALID_ARG, "ctx is NULL");
   if (ctx->desc.weight_dtype != COLIBRI_F32 && ctx->desc.weight_dtype != COLIBRI_BF16)
     return fail(ctx, COLIBRI_ERR_UNSUPPORTED, "colibri_moe_decode needs bf16 or fp32 weights (colibri_moe_forward "
-                "runs quantised layers in one launch at these sizes)");
+                "runs quantised layers)");
   if (T > kFewMaxT) return fail(ctx, COLIBRI_ERR_INVALID_ARG, "T=%d above %d tokens", T, kFewMaxT);
   return forward_impl(ctx, x, T, router_w, router_b, nullptr, nullptr, expert_w, nullptr, shared_w, y, stream, true);
 }
