@@ -185,10 +185,10 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 3 : 2) quantize_ro
 
 template <typename T, int TPR, int kQUnits>
 cudaError_t launch_q(const T* x, int rows, int units, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
-                     const int32_t* dst, int k, cudaStream_t s) {
+                     const int32_t* dst, int k, int sms, cudaStream_t s) {
   constexpr int kRows = kQThreads / TPR;
   // rows loaded ahead: the CTAs that fit on the GPU at once go round (else a CTA takes few rows)
-  const int most = kQUnits <= 2 ? 148 * (sizeof(T) == 2 ? 3 : 2) : 148 * 64;
+  const int most = kQUnits <= 2 ? sms * (sizeof(T) == 2 ? 3 : 2) : sms * 64;
   const int grid = std::min((rows + kRows - 1) / kRows, most);
   return launch_kernel(quantize_rows_kernel<T, TPR, kQUnits>, dim3(grid), dim3(kQThreads), 0, s, 1, x, rows, units, ldx,
                        q, ldq, scale, dst, k);
@@ -199,14 +199,14 @@ cudaError_t launch_q(const T* x, int rows, int units, int64_t ldx, int8_t* q, in
 // spills); longer rows four units on 256 threads.
 template <typename T>
 cudaError_t launch_rows(const T* x, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
-                        const int32_t* dst, int k, cudaStream_t s) {
+                        const int32_t* dst, int k, int sms, cudaStream_t s) {
   const int units = cols / 16;
-  if (units <= 32) return launch_q<T, 32, 1>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
-  if (units <= 64) return launch_q<T, 32, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
-  if (units <= 128) return launch_q<T, 64, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
-  if (units <= 256) return launch_q<T, 128, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
-  if (units <= 512) return launch_q<T, 256, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
-  return launch_q<T, 256, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, s);
+  if (units <= 32) return launch_q<T, 32, 1>(x, rows, units, ldx, q, ldq, scale, dst, k, sms, s);
+  if (units <= 64) return launch_q<T, 32, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, sms, s);
+  if (units <= 128) return launch_q<T, 64, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, sms, s);
+  if (units <= 256) return launch_q<T, 128, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, sms, s);
+  if (units <= 512) return launch_q<T, 256, 2>(x, rows, units, ldx, q, ldq, scale, dst, k, sms, s);
+  return launch_q<T, 256, 4>(x, rows, units, ldx, q, ldq, scale, dst, k, sms, s);
 }
 
 }  // namespace
@@ -214,8 +214,12 @@ cudaError_t launch_rows(const T* x, int rows, int cols, int64_t ldx, int8_t* q, 
 cudaError_t launch_quantize_rows(const void* x, int act, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,
                                  float* scale, cudaStream_t s, const int32_t* dst, int k) {
   if (rows <= 0) return cudaSuccess;
-  if (act == COLIBRI_BF16) return launch_rows((const __nv_bfloat16*)x, rows, cols, ldx, q, ldq, scale, dst, k, s);
-  return launch_rows((const float*)x, rows, cols, ldx, q, ldq, scale, dst, k, s);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  if (act == COLIBRI_BF16) return launch_rows((const __nv_bfloat16*)x, rows, cols, ldx, q, ldq, scale, dst, k, sms, s);
+  return launch_rows((const float*)x, rows, cols, ldx, q, ldq, scale, dst, k, sms, s);
 }
 
 }  // namespace colibri
