@@ -269,8 +269,8 @@ colibri_status colibri_combine(const void* Yp, int32_t act_dtype, const int32_t*
  * and W must start on 16-byte boundaries, those of y need not.  K (cols) is a multiple of 16, up
  * to 131056 (the int32 sums are exact); N up to 2^20, rows up to 2^24; zero rows launch nothing.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA; reason via colibri_last_error(NULL).  A
- * device-side wait that gives up is reported by colibri_int_check.  The first call on each device
- * loads the kernels and should come before any stream capture.
+ * device-side wait that gives up is reported by colibri_int_check.  Calls may be captured into a
+ * graph, the first of a process among them.
  *
  * colibri_quantize_rows -- per row r of x [rows, cols] (act_dtype F32 or BF16):
  *   scale[r] = max |x[r][:]| / 127 in fp32; q[r][c] = the integer nearest to the exact quotient

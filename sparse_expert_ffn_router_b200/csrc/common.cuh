@@ -423,7 +423,7 @@ cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s);
 // dst: nullptr, or [rows, k]: row r's integers and scale go to rows dst[r][0..k) instead of to row r
 cudaError_t launch_quantize_rows(const void* x, int act, int rows, int cols, int64_t ldx, int8_t* q, int64_t ldq,
                                  float* scale, cudaStream_t s, const int32_t* dst = nullptr, int k = 1);
-cudaError_t configure_int_kernels();  // once per device, before any launch inside a stream capture
+cudaError_t configure_int_kernels();  // once per device, before a context's launches
 
 // ---------------------------------------------------------------------------------------
 // Small device helpers

@@ -1150,7 +1150,7 @@ cudaError_t launch_int_gemm(const IntGemmArgs& a, bool swiglu, cudaStream_t s) {
   return swiglu ? launch_pair<true>(a, sms, s) : launch_pair<false>(a, sms, s);
 }
 
-// Loads the kernels a context's forward may launch, so that its first launch may be a captured one.
+// Allows the kernels that a context's forward may launch their shared memory, before the first launch.
 cudaError_t configure_int_kernels() {
   const auto set = [](auto kern, size_t smem) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
