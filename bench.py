@@ -12,10 +12,12 @@ fp32 layer, the Mixtral prefill, the 128-expert layer with a shared expert, the 
 and int8 and group-wise int4 decode at T = 1, 8 and 32): the median time per call over at least
 --calls calls with L2 flushed before each call, the dominant kernel's roofline from the stage
 events of an equal region (recorded inside the replayed CUDA graph), its own clock record, and
-end-to-end figures.
+end-to-end figures.  The printed line holds of each entry what it is read for (time, tokens/s, roofline
+fraction, end-to-end tokens/s, clock), so that it stays below 4000 characters whoever keeps only the end of
+a log; --detail FILE writes the whole record (regions, percentiles, stages, traffic, clocks).
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME] [--workloads all|none|a,b]
-                    [--calls C] [--impl colibri|reference]
+                    [--calls C] [--detail FILE] [--impl colibri|reference]
 
 With --gpus N > 1 (launched by torch.distributed.run) every rank runs an independent replica
 of the workload on its own GPU (weak scaling; the layer has no exchange step when tokens
@@ -92,6 +94,7 @@ def parse():
     ap.add_argument("--workloads", default="all",
                     help="workloads measured in the line's `workloads` object: all, none, or a comma list")
     ap.add_argument("--calls", type=int, default=100, help="minimum calls per `workloads` entry")
+    ap.add_argument("--detail", default=None, help="file that the whole record is written to")
     a = ap.parse_args()
     a.warmup = max(a.warmup, 3)
     return a
@@ -567,6 +570,42 @@ def measure_entry(wl, a, local, world, pk):
         r.close()
 
 
+# What the printed line keeps of each part of the record.
+LINE_PARTS = {
+    "roofline": ("kernel", "bound", "achieved", "peak", "unit", "frac", "peak_source", "traffic"),
+    "e2e": ("value", "unit", "h2d_bytes_per_step", "d2h_bytes_per_step", "us_per_call", "pipelined_value"),
+    "clocks": ("sm_mhz", "sm_max_mhz", "reasons"),
+    "cpu_baseline": ("value", "unit", "cores", "kind"),
+}
+LINE_DROPS = ("clocks_profiled", "profiled_over_timed", "stage_timing", "routing_counts")
+ENTRY_PARTS = {"us_per_call": None, "tokens_per_s": None, "roofline": ("bound", "frac"), "e2e": ("value",),
+               "clocks": ("sm_mhz", "reasons")}
+
+
+def rounded(v, digits):
+    """v with every float in it rounded to `digits` significant digits."""
+    if isinstance(v, float):
+        return float(f"{v:.{digits}g}")
+    if isinstance(v, dict):
+        return {k: rounded(x, digits) for k, x in v.items()}
+    return [rounded(x, digits) for x in v] if isinstance(v, list) else v
+
+
+def printed(record):
+    """The line that is printed for a record: its contract fields whole, the rest in short."""
+    line = {k: v for k, v in record.items() if k not in LINE_DROPS and k != "workloads"}
+    for part, keys in LINE_PARTS.items():
+        if part in line:
+            line[part] = {k: line[part][k] for k in keys if k in line[part]}
+    line = rounded(line, 8)
+    if "workloads" in record:
+        line["workloads"] = {
+            name: rounded({part: entry[part] if keys is None else {k: entry[part][k] for k in keys}
+                           for part, keys in ENTRY_PARTS.items()}, 5)
+            for name, entry in record["workloads"].items()}
+    return json.dumps(line, separators=(",", ":"))
+
+
 def main():
     a = parse()
     rank = int(os.environ.get("RANK", "0"))
@@ -648,7 +687,10 @@ def main():
             torch.cuda.empty_cache()
         line["workloads"] = entries
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        if a.detail:
+            with open(a.detail, "w") as f:
+                json.dump(line, f)
+        print(printed(line), flush=True)
     if world > 1:
         dist.barrier()
         dist.destroy_process_group()
