@@ -34,14 +34,15 @@
 // row feed two instructions as they are, and the token operand is 16 bytes of the token's row.  fp32:
 // FMA on the CUDA cores.  H is kept as fp32, or as two bf16 (its rounding and what that left, 2^-16 in
 // all): one rounding to bf16 would double the variance of the output's own rounding error (0.0023
-// against 0.0017 of the output's norm); the second product costs 4 us of 70 on 128 small experts and
-// nothing measurable on large ones.
+// against 0.0017 of the output's norm); the second product and its sums, kept apart, cost 5 us of 67 on 128
+// small experts, 1 of 122 at one token of large ones and nothing at 16.
 //
-// Measured (B200, copy bandwidth 6455 GB/s): d = 4096, f = 14336, 8 experts, top-2, bf16: 1 token (704 MB)
-// 120 us, 5.9 TB/s; 16 tokens (2.8 GB) 461 us, 6.1 TB/s.  128 experts of d = 2048, f = 768, top-4, with a
-// shared expert of 1536: 8 tokens (291 MB) 69 us.  An fp32 layer of 256 x 512: 16.5 us, latency alone
-// (logits 2.5, selection 1.8, gate/up 4, down 2, the barriers 2 each, the launch 3).  fp32 with many tokens
-// is bound by the lanes' exchanges and FMAs: two experts of 1024 x 2688 (66 MB) 24 us at one token, 64 at 16.
+// Measured (B200, copy bandwidth 6455 GB/s; 20 calls in a row, a call by itself is 1 to 4 % slower): d = 4096,
+// f = 14336, 8 experts, top-2, bf16: 1 token (704 MB) 122 us, 5.8 TB/s; 16 tokens (2.8 GB) 453 us, 6.2 TB/s.
+// 128 experts of d = 2048, f = 768, top-4, with a shared expert of 1536: 8 tokens (291 MB) 67.5 us.  An fp32
+// layer of 256 x 512: 16.5 us, latency alone (logits 2.5, selection 1.8, gate/up 4, down 2, the barriers 2
+// each, the launch 3).  fp32 with many tokens is bound by the lanes' exchanges and FMAs: two experts of
+// 1024 x 2688 (66 MB) 23 us at one token, 37 at 8, 65 at 16.
 #include "common.cuh"
 
 namespace colibri {

