@@ -313,7 +313,8 @@ colibri_status colibri_int_gemm_experts(const int8_t* A, int64_t lda, const floa
 /*
  * colibri_int_swiglu_experts -- the gate and up projections in one call: expert e holds
  * W1 [N, K] | W3 [N, K] and scales s1 [N] | s3 [N] (the start of the expert weight buffer's int8
- * layout); g and u are the two products in fp32 and h[r][n] = silu(g) * u.  Other arguments as
+ * layout); g and u are the two products in fp32 and h[r][n] = silu(g) * u, where a silu(g) below
+ * 1.1e-36 in magnitude (g below -87) may count as zero.  Other arguments as
  * colibri_int_gemm_experts.
  */
 colibri_status colibri_int_swiglu_experts(const int8_t* A, int64_t lda, const float* a_scale,
